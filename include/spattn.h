@@ -53,10 +53,13 @@ typedef enum {
     SPATTN_ERR_BAD_CSR = 3,     /* CSR/COO content invalid (see spattn_create_csr_mask) */
     SPATTN_ERR_CUDA = 4,        /* a CUDA runtime call failed; spattn_last_error() names it */
     SPATTN_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up */
-    SPATTN_ERR_OOM = 6          /* device memory allocation failed */
+    SPATTN_ERR_OOM = 6,         /* device memory allocation failed */
+    SPATTN_ERR_BAD_CACHE = 7    /* a cache call left places out or met values it cannot hold (see spattn_device_error) */
 } spattn_status;
 
-typedef enum { SPATTN_BF16 = 0, SPATTN_F32 = 1 } spattn_dtype;
+/* I8 and E4M3 (8-bit floats: 4 exponent and 3 mantissa bits, no infinities) are
+ * the types of a cache's codes only (spattn_cache). */
+typedef enum { SPATTN_BF16 = 0, SPATTN_F32 = 1, SPATTN_I8 = 2, SPATTN_E4M3 = 3 } spattn_dtype;
 
 /* A strided 4-D view of device memory. Strides are in elements. A dimension of
  * size 1 may have any stride (it is read as 0, i.e. broadcast). */
@@ -362,6 +365,89 @@ int spattn_fwd_noalloc(const spattn_tensor* q, const spattn_tensor* k, const spa
                        int64_t nnz, const spattn_tensor* add_mask, const spattn_tensor* bias,
                        float scale, const spattn_tensor* out, float* lse, void* stream);
 
+/* ------------------------------------------------- 8-bit key/value cache */
+
+/* A key/value cache held in 8 bits, in pages. Generating token by token, a
+ * model keeps the keys and values of the tokens so far; in 8 bits with a scale
+ * for each page and head they take half the memory, and half the time to read,
+ * of bf16 values.
+ *   k, v        [num_pages, Hk, page, d] codes, both SPATTN_I8 or both
+ *               SPATTN_E4M3; page a power of two in 16..256, d in {32, 64, 128};
+ *               stride 1 over d, base pointers and strides multiples of 16 bytes.
+ *               (A [num_pages, page, Hk, d] pool is a view with other strides.)
+ *   k_scale, v_scale  device float [num_pages, Hk], contiguous, >= 0: a code c of
+ *               page x and head h stands for the fp32 product c * scale[x, h].
+ *   page_table  device int32 [batch, max_pages], rows table_stride elements apart:
+ *               token j of sequence b lies in page page_table[b, j / page], at
+ *               place j % page. Entries behind a sequence's last page are not
+ *               read. An entry outside [0, num_pages) that a call does need is
+ *               left out (its tokens are not written, read as zeros, not
+ *               attended to) and raises device error flag bit 2.
+ * Sequences may share pages that are only read (a common prefix). Pages that a
+ * call writes must each belong to one sequence: two that write the same page in
+ * one call leave its codes unspecified. */
+typedef struct {
+    spattn_tensor k, v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;
+    int32_t batch, max_pages;
+    int64_t table_stride;
+} spattn_cache;
+
+/* Quantise new tokens into the cache. k, v: [batch, Hk, m, d], bf16 or f32 (both
+ * the same), strides as spattn_fwd's. Token t < length[b] of sequence b goes to
+ * place start[b] + t (start, length: device int32 [batch]; start NULL: 0 for
+ * every sequence, length NULL: m; lengths are clamped to [0, m]). Per touched
+ * page and head, for K and for V:
+ *   a    = max |x| over the call's tokens in the page
+ *   s    = a / qmax (qmax 127 for I8, 448 for E4M3), in fp32. A page that
+ *          already holds older tokens of the sequence (places before start[b])
+ *          keeps its scale when that is larger.
+ *   code = x / s, an fp32 quotient rounded to the nearest code (ties to even);
+ *          0 when s is 0.
+ * When the scale of a page with older tokens grows, their codes become
+ * (code * s_old) / s, rounded the same way. Codes behind the last new token stay
+ * as they are. Writing the same tokens to the same places again changes nothing.
+ * A NaN is written as 0 and an infinity as the largest code of its sign, neither
+ * counts in a, and both raise device error flag bit 3. A sequence whose tokens do
+ * not all lie in [0, max_pages * page) is left out whole and raises bit 2.
+ * Stream-ordered, never synchronises, allocates nothing. Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int spattn_cache_write(const spattn_tensor* k, const spattn_tensor* v, const spattn_cache* cache,
+                       const int32_t* start, const int32_t* length, void* stream);
+
+/* Read tokens back: k, v [batch, Hk, m, d] (bf16 or f32, both the same) get the
+ * values of the places start[b] + t, t < length[b], rounded to nearest even, and
+ * zeros for t >= length[b] and for places without a page (which raise device
+ * error flag bit 2). start, length as spattn_cache_write's. The values are what
+ * spattn_fwd_cache attends to; with k and v given to spattn_fwd_mask_kpad a
+ * whole cached sequence can run under any mask. Stream-ordered, never
+ * synchronises, allocates nothing. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int spattn_cache_read(const spattn_cache* cache, const int32_t* start, const int32_t* length,
+                      const spattn_tensor* k, const spattn_tensor* v, void* stream);
+
+/* Attention of each sequence's last tokens over its cache.
+ *   q        [batch, H, m, d], bf16 or f32, strides as spattn_fwd's; H a multiple
+ *            of Hk: query heads h .. of one group of H / Hk share K/V head h / (H / Hk).
+ *   seqlen   device int32 [batch]: tokens in the cache, those of the queries among
+ *            them (written before this call); clamped to [0, max_pages * page].
+ *   qlen     device int32 [batch], or NULL (m for every sequence): queries of
+ *            sequence b, clamped to [0, m]. Query t < qlen[b] is token
+ *            pos = seqlen[b] - qlen[b] + t.
+ *   window   < 0: query t attends to every token j <= pos. >= 0: to those with
+ *            j >= pos - window, and to the global tokens j < n_global (>= 0):
+ *            the causal half of a sliding-window mask with global tokens.
+ *   scale, out, lse  as spattn_fwd's; out [batch, H, m, d], lse[(b*H + h)*m + t].
+ * Rows without a token (t >= qlen[b], or pos < 0) give out = 0 and lse = -inf.
+ * Tokens at and behind seqlen[b] are never used, whatever their codes; a token
+ * whose codes are NaN (E4M3 only; spattn_cache_write writes none) must not be
+ * attended to by any query of the call. Stream-ordered, never synchronises;
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
+int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const int32_t* seqlen,
+                     const int32_t* qlen, int32_t window, int32_t n_global, float scale,
+                     const spattn_tensor* out, float* lse, void* stream);
+
 /* ------------------------------------------------------------- utilities */
 
 /* Message of the last failed call on this thread ("" if none). Valid until the
@@ -371,16 +457,19 @@ const char* spattn_last_error(void);
 /* Synchronise `stream`, then read and clear the current device's error flags
  * raised by kernels (bit 0: a column index outside [0, n) was skipped, or an
  * asynchronous interval-mask build met a negative half-width; bit 1:
- * a bounded wait in the tensor-core kernel expired and its rows are invalid).
- * *flags may be NULL. Returns SPATTN_OK, SPATTN_ERR_TIMEOUT if bit 1 was set,
- * else SPATTN_ERR_BAD_CSR if bit 0 was set. */
+ * a bounded wait in the tensor-core kernel expired and its rows are invalid;
+ * bit 2: a cache call left out places that have no page; bit 3: a NaN or an
+ * infinity was written to a cache). *flags may be NULL. Returns SPATTN_OK,
+ * SPATTN_ERR_TIMEOUT if bit 1 was set, else SPATTN_ERR_BAD_CSR if bit 0 was set,
+ * else SPATTN_ERR_BAD_CACHE if bit 2 or 3 was set. */
 int spattn_device_error(void* stream, uint32_t* flags);
 
 /* spattn_device_error without the flag word: synchronises `stream`, reads and
  * clears the error flags, and returns SPATTN_ERR_TIMEOUT if a bounded
  * device-side wait expired, SPATTN_ERR_BAD_CSR if a column outside [0, n) was
- * skipped (or an asynchronous build met a negative half-width), SPATTN_OK
- * otherwise (SPATTN_ERR_CUDA if the synchronisation itself fails). */
+ * skipped (or an asynchronous build met a negative half-width),
+ * SPATTN_ERR_BAD_CACHE if a cache call left out places or met values it cannot
+ * hold (bits 2 and 3 of spattn_device_error), SPATTN_OK otherwise (SPATTN_ERR_CUDA if the synchronisation itself fails). */
 int spattn_check_device_error(void* stream);
 
 /* Library version: major * 10000 + minor * 100 + patch. */

@@ -27,12 +27,15 @@ SPATTN_ERR_BAD_CSR = 3
 SPATTN_ERR_CUDA = 4
 SPATTN_ERR_TIMEOUT = 5
 SPATTN_ERR_OOM = 6
+SPATTN_ERR_BAD_CACHE = 7
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "BAD_CSR", 4: "CUDA",
-                5: "TIMEOUT", 6: "OOM"}
+                5: "TIMEOUT", 6: "OOM", 7: "BAD_CACHE"}
 
 # spattn_dtype
 SPATTN_BF16 = 0
 SPATTN_F32 = 1
+SPATTN_I8 = 2
+SPATTN_E4M3 = 3
 
 # spattn_mask_kind
 SPATTN_MASK_CSR = 0
@@ -66,6 +69,13 @@ class spattn_mask_spec(ctypes.Structure):
                 ("half_widths", ctypes.c_void_p), ("in_row_ptr", ctypes.c_void_p),
                 ("in_col_idx", ctypes.c_void_p), ("in_nnz", ctypes.c_int64),
                 ("tile_min_nnz", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class spattn_cache(ctypes.Structure):
+    _fields_ = [("k", spattn_tensor), ("v", spattn_tensor), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -102,6 +112,10 @@ SIGNATURES = {
                                           _TP, ctypes.c_float, _TP, _P, _P]),
     "spattn_bwd_mask": (ctypes.c_int, [_TP, _TP, _TP, _P, _TP, _TP, ctypes.c_float, _TP, _P, _TP, _TP,
                                        _TP, _TP, _TP, _P]),
+    "spattn_cache_write": (ctypes.c_int, [_TP, _TP, ctypes.POINTER(spattn_cache), _P, _P, _P]),
+    "spattn_cache_read": (ctypes.c_int, [ctypes.POINTER(spattn_cache), _P, _P, _TP, _TP, _P]),
+    "spattn_fwd_cache": (ctypes.c_int, [_TP, ctypes.POINTER(spattn_cache), _P, _P, ctypes.c_int32,
+                                        ctypes.c_int32, ctypes.c_float, _TP, _P, _P]),
     "spattn_version": (ctypes.c_int, []),
     "spattn_launch_count": (ctypes.c_uint64, []),
     "spattn_alloc_count": (ctypes.c_uint64, []),
@@ -365,17 +379,17 @@ def spattn_device_error(stream=None) -> int:
     """Synchronise the stream; return (and clear) the kernels' error flag bits."""
     flags = ctypes.c_uint32()
     st = LIB.spattn_device_error(_stream(stream), ctypes.byref(flags))
-    if st not in (SPATTN_OK, SPATTN_ERR_BAD_CSR):
+    if st not in (SPATTN_OK, SPATTN_ERR_BAD_CSR, SPATTN_ERR_BAD_CACHE):
         _check(st)
     return flags.value
 
 
 def spattn_check_device_error(stream=None) -> int:
     """Synchronise the stream, clear the kernels' error flags and return the
-    status they map to (SPATTN_OK, SPATTN_ERR_TIMEOUT or SPATTN_ERR_BAD_CSR);
-    raises only when the synchronisation itself fails."""
+    status they map to (SPATTN_OK, SPATTN_ERR_TIMEOUT, SPATTN_ERR_BAD_CSR or
+    SPATTN_ERR_BAD_CACHE); raises only when the synchronisation itself fails."""
     st = LIB.spattn_check_device_error(_stream(stream))
-    if st not in (SPATTN_OK, SPATTN_ERR_BAD_CSR, SPATTN_ERR_TIMEOUT):
+    if st not in (SPATTN_OK, SPATTN_ERR_BAD_CSR, SPATTN_ERR_TIMEOUT, SPATTN_ERR_BAD_CACHE):
         _check(st)
     return st
 
@@ -450,6 +464,135 @@ def spattn_bwd_mask(q, k, v, mask: "Mask", out, lse, dout, add_mask=None, bias=N
                                ctypes.byref(ds[6]), ctypes.byref(ds[7]),
                                ctypes.byref(ddb) if ddb is not None else None, _stream(stream)))
     return dq, dk, dv, dbias
+
+
+# ------------------------------------------------------- 8-bit key/value cache
+class Cache:
+    """A paged key/value cache held in 8 bits (``spattn_cache``): the tensors and
+    their description for the library. The tensors stay the caller's; a Cache
+    keeps them alive and reads their addresses once, so rebind it to new tensors
+    by making a new one (their contents may change freely between calls).
+
+    ``k``, ``v``: [num_pages, Hk, page, d], both ``torch.int8`` or both
+    ``torch.float8_e4m3fn``, any strides with stride 1 over d.
+    ``k_scale``, ``v_scale``: float32 [num_pages, Hk], contiguous.
+    ``page_table``: int32 [batch, max_pages]; row b lists the pages of sequence b."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table):
+        import torch
+        for name, t, dt, dim in (("k", k, None, 4), ("v", v, None, 4), ("k_scale", k_scale, torch.float32, 2),
+                                 ("v_scale", v_scale, torch.float32, 2),
+                                 ("page_table", page_table, torch.int32, 2)):
+            if t.dim() != dim:
+                raise ValueError(f"cache {name} is {dim}-D")
+            if dt is not None and t.dtype != dt:
+                raise ValueError(f"cache {name} must be {dt}, not {t.dtype}")
+            if t.device != k.device:
+                raise ValueError(f"cache {name} is on {t.device}, k on {k.device}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if tuple(t.shape) != tuple(k.shape[:2]) or not t.is_contiguous():
+                raise ValueError(f"cache {name} must be a contiguous [num_pages, Hk] tensor")
+        if page_table.stride(1) != 1 and page_table.shape[1] > 1:
+            raise ValueError("cache page_table rows must be contiguous")
+        codes = {torch.int8: SPATTN_I8, torch.float8_e4m3fn: SPATTN_E4M3}
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype not in codes:
+                raise ValueError(f"cache {name}: unsupported dtype {t.dtype}")
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.device = k.device
+        self.heads, self.page, self.d = k.shape[1:]
+        self.batch, self.max_pages = page_table.shape
+        self.desc = spattn_cache(_fill_desc(k, codes[k.dtype]), _fill_desc(v, codes[v.dtype]),
+                                 k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+                                 self.batch, self.max_pages, page_table.stride(0))
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page: int, d: int, page_table, dtype=None):
+        """A cache of its own pages, on page_table's device. ``dtype``:
+        ``torch.float8_e4m3fn`` (default) or ``torch.int8``."""
+        import torch
+        dtype = torch.float8_e4m3fn if dtype is None else dtype
+        dev = page_table.device
+        k, v = (torch.zeros((num_pages, heads, page, d), dtype=torch.int8, device=dev).view(dtype) for _ in range(2))
+        ks, vs = (torch.zeros((num_pages, heads), dtype=torch.float32, device=dev) for _ in range(2))
+        return cls(k, v, ks, vs, page_table)
+
+
+def _fill_desc(t, code: int) -> spattn_tensor:
+    return spattn_tensor(t.data_ptr(), code, 0, tuple(t.shape), t.stride())
+
+
+def _lens(t, name: str, cache: Cache) -> Optional[int]:
+    """Address of an int32 [batch] tensor on the cache's device (or None)."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != cache.batch or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [batch] tensor")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return t.data_ptr()
+
+
+def _beside(t, name: str, cache: Cache) -> spattn_tensor:
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return tensor_desc(t)
+
+
+def _on(cache: Cache, stream):
+    """The stream of a cache call (default: the current stream of the cache's
+    device) and a context in which the cache's device is current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    return _stream(stream), torch.cuda.device(cache.device)
+
+
+def spattn_cache_write(k, v, cache: Cache, start=None, length=None, stream=None) -> None:
+    """Quantise the tokens k, v [batch, Hk, m, d] into the cache: token
+    t < length[b] goes to place start[b] + t (int32 [batch] tensors; None: 0, and m)."""
+    dk, dv = _beside(k, "k", cache), _beside(v, "v", cache)
+    st, ln = _lens(start, "start", cache), _lens(length, "length", cache)
+    s, on = _on(cache, stream)
+    with on:
+        _check(LIB.spattn_cache_write(ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(cache.desc), st, ln, s))
+
+
+def spattn_cache_read(cache: Cache, m: int, dtype=None, start=None, length=None, k=None, v=None, stream=None):
+    """The values of the places start[b] + t, t < length[b], as k, v
+    [batch, Hk, m, d] (``dtype``: bfloat16, the default, or float32; zeros
+    behind length[b]). Outputs may be given as ``k`` and ``v``."""
+    import torch
+    shape = (cache.batch, cache.heads, m, cache.d)
+    dtype = torch.bfloat16 if dtype is None else dtype
+    k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+    dk, dv = _beside(k, "k", cache), _beside(v, "v", cache)
+    if k.shape[2] != m:
+        raise ValueError(f"k holds {k.shape[2]} tokens, not {m}")
+    st, ln = _lens(start, "start", cache), _lens(length, "length", cache)
+    s, on = _on(cache, stream)
+    with on:
+        _check(LIB.spattn_cache_read(ctypes.byref(cache.desc), st, ln, ctypes.byref(dk), ctypes.byref(dv), s))
+    return k, v
+
+
+def spattn_fwd_cache(q, cache: Cache, seqlen, qlen=None, window: int = -1, n_global: int = 0,
+                     scale: Optional[float] = None, out=None, lse=None, want_lse: bool = True, stream=None):
+    """Attention of each sequence's last qlen[b] (None: m) tokens, q
+    [batch, H, m, d], over the seqlen[b] tokens of its cache (int32 [batch]
+    tensors). ``window`` >= 0: only the last window + 1 tokens and the first
+    ``n_global``. Returns (out [batch, H, m, d], lse [batch*H*m] or None)."""
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    out, lse = _outputs(q, out, lse, want_lse)
+    dq, do = _beside(q, "q", cache), _beside(out, "out", cache)
+    sl, ql = _lens(seqlen, "seqlen", cache), _lens(qlen, "qlen", cache)
+    s, on = _on(cache, stream)
+    with on:
+        _check(LIB.spattn_fwd_cache(ctypes.byref(dq), ctypes.byref(cache.desc), sl, ql, window, n_global,
+                                    float(scale), ctypes.byref(do), _ptr(lse), s))
+    return out, lse
 
 
 def spattn_version() -> int:

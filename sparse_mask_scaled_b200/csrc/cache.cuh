@@ -1,0 +1,94 @@
+// The 8-bit key/value cache: what its kernels (cache.cu, fwd_cache.cu) and the
+// C ABI share.
+//
+// A cache is a pool of pages, each `page` tokens (a power of two) of every
+// key/value head. The codes of page x, head h, token o are d consecutive bytes;
+// a code c of page x and head h stands for the fp32 product c * scale[x, h]. Row
+// b of the page table lists the pages of sequence b: token j lies in page
+// table[b, j / page] at place j % page.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "spattn_internal.cuh"
+
+namespace spattn {
+
+constexpr int kCodeI8 = 0;
+constexpr int kCodeE4m3 = 1;
+constexpr int kMinPage = 16, kMaxPage = 256;
+
+struct CacheSide {  // K or V
+    uint8_t* codes;
+    float* scale;           // [num_pages, Hk]
+    int64_t s_p, s_h, s_t;  // bytes between pages, heads, tokens
+};
+
+struct CacheView {
+    CacheSide k, v;
+    const int32_t* table;  // [B, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int B, max_pages, num_pages, Hk, page_shift;
+    unsigned* err;  // device error flags
+};
+
+// The page of sequence b that holds token j, or -1 (flagged) when the table
+// names none of the pool's pages. Callers pass only tokens that have a place in
+// the table.
+__device__ __forceinline__ int cache_page(const CacheView& c, int b, int64_t j) {
+    const int p = __ldg(c.table + b * c.table_stride + (j >> c.page_shift));
+    if ((unsigned)p < (unsigned)c.num_pages) return p;
+    atomicOr(c.err, kErrBadPage);
+    return -1;
+}
+
+// Tokens sequence b can hold.
+__device__ __forceinline__ int64_t cache_capacity(const CacheView& c) {
+    return (int64_t)c.max_pages << c.page_shift;
+}
+
+template <int CODE>
+__device__ __forceinline__ float code_value(unsigned byte) {
+    if constexpr (CODE == kCodeI8) {
+        return (float)(int8_t)byte;
+    } else {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
+        return __half2float(__half(h));
+    }
+}
+
+template <int CODE>
+constexpr float code_max() {
+    return CODE == kCodeI8 ? 127.f : 448.f;
+}
+
+// Entry points of cache.cu. real: 0 bf16, 1 f32; code: kCodeI8 or kCodeE4m3.
+struct CacheRows {  // K and V as [B, Hk, m, d]; strides in elements
+    void* k;
+    void* v;
+    int64_t k_sb, k_sh, k_sn, v_sb, v_sh, v_sn;
+    int m;
+    const int32_t* start;   // nullable (all 0)
+    const int32_t* length;  // nullable (all m)
+};
+cudaError_t launch_cache_write(const CacheView& c, const CacheRows& r, int real, int code, int d, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheView& c, const CacheRows& r, int real, int code, int d, cudaStream_t s);
+
+// Entry point of fwd_cache.cu.
+struct CacheFwdParams {
+    CacheView c;
+    const void* q;
+    void* out;
+    float* lse;  // nullable, [B * H * m]
+    int64_t q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
+    int B, H, G, m;         // G query heads share a key/value head
+    const int32_t* seqlen;  // [B]
+    const int32_t* qlen;    // nullable (all m)
+    int window;             // < 0: none
+    int n_global;
+    float scale_log2;  // scale * log2(e)
+};
+cudaError_t launch_fwd_cache(const CacheFwdParams& p, int real, int code, int d, cudaStream_t s);
+
+}  // namespace spattn

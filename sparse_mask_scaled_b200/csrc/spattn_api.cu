@@ -1,13 +1,14 @@
 // C ABI of libspattn: argument checks, the stream-ordered memory pool, mask
 // handles and kernel launches. Every numerical step runs in the kernels of
-// fwd_gather.cu, fwd_tc.cu, mask_build.cu and plan.cu; this file only validates
-// and schedules.
+// fwd_gather.cu, fwd_tc.cu, mask_build.cu, plan.cu, cache.cu and fwd_cache.cu;
+// this file only validates and schedules.
 //
 // Argument checks run before any CUDA call, so a rejected call touches no
 // device state.
 #include "spattn.h"
 #include "spattn_internal.cuh"
 #include "bsg_plan.cuh"
+#include "cache.cuh"
 
 #include <stdarg.h>
 #include <stdio.h>
@@ -1381,6 +1382,123 @@ int create_mask(const spattn_mask_spec* spec, void* stream_v, spattn_mask* out, 
     return SPATTN_OK;
 }
 
+// ------------------------------------------------- 8-bit key/value cache
+
+int check_cache_side(const spattn_tensor* t, const char* name, const int64_t* shape, int32_t dtype,
+                     const float* scale, CacheSide* out) {
+    if (t->reserved != 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.%s.reserved must be 0", name);
+    if (t->dtype != dtype) return fail(SPATTN_ERR_INVALID_ARG, "cache.%s dtype %d differs from k's %d", name, t->dtype, dtype);
+    for (int x = 0; x < 4; ++x)
+        if (t->shape[x] != shape[x])
+            return fail(SPATTN_ERR_INVALID_ARG, "cache.%s shape[%d] = %lld, expected %lld", name, x,
+                        (long long)t->shape[x], (long long)shape[x]);
+    if (!t->data) return fail(SPATTN_ERR_INVALID_ARG, "cache.%s.data is NULL", name);
+    if (!scale) return fail(SPATTN_ERR_INVALID_ARG, "cache.%s_scale is NULL", name);
+    if (((uintptr_t)scale) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.%s_scale not aligned", name);
+    if (t->stride[3] != 1) return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s needs stride 1 over d", name);
+    if (((uintptr_t)t->data) % 16 != 0)
+        return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s.data is not 16-byte aligned", name);
+    for (int x = 0; x < 3; ++x)
+        if (t->shape[x] > 1 && (t->stride[x] % 16 != 0 || t->stride[x] < 0))
+            return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s stride[%d] is negative or not a multiple of 16 bytes", name, x);
+    auto bs = [&](int x) { return t->shape[x] == 1 ? 0 : t->stride[x]; };
+    out->codes = static_cast<uint8_t*>(t->data);
+    out->scale = const_cast<float*>(scale);
+    out->s_p = bs(0);
+    out->s_h = bs(1);
+    out->s_t = bs(2);
+    return SPATTN_OK;
+}
+
+// Argument checks of a cache; fills all of *v but err.
+int check_cache(const spattn_cache* c, CacheView* v, int* code, int* d) {
+    if (!c) return fail(SPATTN_ERR_INVALID_ARG, "cache is NULL");
+    memset(v, 0, sizeof *v);
+    if (c->k.dtype != SPATTN_I8 && c->k.dtype != SPATTN_E4M3)
+        return fail(SPATTN_ERR_UNSUPPORTED, "cache.k dtype %d (supported: SPATTN_I8, SPATTN_E4M3)", c->k.dtype);
+    const int64_t* sh = c->k.shape;
+    for (int x = 0; x < 4; ++x)
+        if (sh[x] < 1 || sh[x] > 0x7fffffff)
+            return fail(SPATTN_ERR_INVALID_ARG, "cache.k shape[%d] = %lld", x, (long long)sh[x]);
+    if (sh[3] != 32 && sh[3] != 64 && sh[3] != 128)
+        return fail(SPATTN_ERR_UNSUPPORTED, "head dim %lld (supported: 32, 64, 128)", (long long)sh[3]);
+    if (sh[2] < kMinPage || sh[2] > kMaxPage || (sh[2] & (sh[2] - 1)) != 0)
+        return fail(SPATTN_ERR_UNSUPPORTED, "page of %lld tokens (supported: powers of two in %d..%d)",
+                    (long long)sh[2], kMinPage, kMaxPage);
+    if (c->batch < 0 || c->max_pages < 1)
+        return fail(SPATTN_ERR_INVALID_ARG, "cache batch %d, max_pages %d", c->batch, c->max_pages);
+    if ((int64_t)c->max_pages * sh[2] > 0x7ffffffe)
+        return fail(SPATTN_ERR_UNSUPPORTED, "max_pages * page above 2^31 - 2 tokens");
+    if ((int64_t)c->batch * sh[1] > 0x7fffffff) return fail(SPATTN_ERR_UNSUPPORTED, "batch * Hk too large");
+    if (!c->page_table) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table is NULL");
+    if (((uintptr_t)c->page_table) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table not aligned");
+    if (c->batch > 1 && c->table_stride < c->max_pages)
+        return fail(SPATTN_ERR_INVALID_ARG, "cache.table_stride %lld < max_pages %d", (long long)c->table_stride,
+                    c->max_pages);
+    int r;
+    if ((r = check_cache_side(&c->k, "k", sh, c->k.dtype, c->k_scale, &v->k))) return r;
+    if ((r = check_cache_side(&c->v, "v", sh, c->k.dtype, c->v_scale, &v->v))) return r;
+    v->table = c->page_table;
+    v->table_stride = c->batch > 1 ? c->table_stride : 0;
+    v->B = c->batch;
+    v->max_pages = c->max_pages;
+    v->num_pages = (int)sh[0];
+    v->Hk = (int)sh[1];
+    while ((1 << v->page_shift) < sh[2]) ++v->page_shift;
+    *code = c->k.dtype == SPATTN_I8 ? kCodeI8 : kCodeE4m3;
+    *d = (int)sh[3];
+    return SPATTN_OK;
+}
+
+// A [batch, heads, m, d] tensor beside a cache.
+int check_cache_rows(const spattn_tensor* t, const char* name, const CacheView& v, int64_t heads, int64_t m, int d,
+                     int32_t dtype) {
+    const int64_t shape[4] = {v.B, heads, m, d};
+    return check_qkv(t, name, shape, dtype);
+}
+
+int check_lens(const int32_t* p, const char* name) {
+    if (((uintptr_t)p) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "%s not aligned", name);
+    return SPATTN_OK;
+}
+
+// spattn_cache_write and spattn_cache_read.
+int cache_rows(const spattn_tensor* k, const spattn_tensor* v, const spattn_cache* cache, const int32_t* start,
+               const int32_t* length, void* stream_v, bool write) {
+    g_msg[0] = 0;
+    CacheView c;
+    int code, d, r;
+    if ((r = check_cache(cache, &c, &code, &d))) return r;
+    if (!k) return fail(SPATTN_ERR_INVALID_ARG, "k is NULL");
+    if (!dtype_ok(k->dtype)) return fail(SPATTN_ERR_UNSUPPORTED, "k dtype %d", k->dtype);
+    const int64_t m = k->shape[2];
+    if (m < 0 || m > 0x7ffffffe) return fail(SPATTN_ERR_INVALID_ARG, "k shape[2] = %lld", (long long)m);
+    if ((r = check_cache_rows(k, "k", c, c.Hk, m, d, k->dtype))) return r;
+    if ((r = check_cache_rows(v, "v", c, c.Hk, m, d, k->dtype))) return r;
+    if ((r = check_lens(start, "start"))) return r;
+    if ((r = check_lens(length, "length"))) return r;
+    if (write && (int64_t)c.B * c.Hk * 2 * (m / (1 << c.page_shift) + 2) > 0x7fffffff)
+        return fail(SPATTN_ERR_UNSUPPORTED, "more than 2^31 - 1 pages and heads in one write");
+    if ((int64_t)c.B * m == 0) return SPATTN_OK;
+    cudaStream_t s = (cudaStream_t)stream_v;
+    int dev;
+    CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
+    if ((r = err_flags_ptr(dev, &c.err))) return r;
+    auto bs = [](const spattn_tensor* t, int x) { return t->shape[x] == 1 ? 0 : t->stride[x]; };
+    CacheRows rows;
+    rows.k = k->data;
+    rows.v = v->data;
+    rows.k_sb = bs(k, 0); rows.k_sh = bs(k, 1); rows.k_sn = bs(k, 2);
+    rows.v_sb = bs(v, 0); rows.v_sh = bs(v, 1); rows.v_sn = bs(v, 2);
+    rows.m = (int)m;
+    rows.start = start;
+    rows.length = length;
+    const int real = k->dtype == SPATTN_BF16 ? 0 : 1;
+    const cudaError_t e = write ? launch_cache_write(c, rows, real, code, d, s) : launch_cache_read(c, rows, real, code, d, s);
+    if (e != cudaSuccess) return cuda_fail(e, write ? "cache write launch" : "cache read launch");
+    return SPATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1902,6 +2020,65 @@ int spattn_fwd_noalloc(const spattn_tensor* q, const spattn_tensor* k, const spa
     return launch_fwd(p, dtype, d, sms, s);
 }
 
+int spattn_cache_write(const spattn_tensor* k, const spattn_tensor* v, const spattn_cache* cache,
+                       const int32_t* start, const int32_t* length, void* stream_v) {
+    return cache_rows(k, v, cache, start, length, stream_v, true);
+}
+
+int spattn_cache_read(const spattn_cache* cache, const int32_t* start, const int32_t* length,
+                      const spattn_tensor* k, const spattn_tensor* v, void* stream_v) {
+    return cache_rows(k, v, cache, start, length, stream_v, false);
+}
+
+int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const int32_t* seqlen,
+                     const int32_t* qlen, int32_t window, int32_t n_global, float scale,
+                     const spattn_tensor* out, float* lse, void* stream_v) {
+    g_msg[0] = 0;
+    CacheFwdParams p;
+    memset(&p, 0, sizeof p);
+    int code, d, r;
+    if ((r = check_cache(cache, &p.c, &code, &d))) return r;
+    if (!q) return fail(SPATTN_ERR_INVALID_ARG, "q is NULL");
+    if (!dtype_ok(q->dtype)) return fail(SPATTN_ERR_UNSUPPORTED, "q dtype %d", q->dtype);
+    const int64_t H = q->shape[1], m = q->shape[2];
+    if (H < 1 || H % p.c.Hk != 0)
+        return fail(SPATTN_ERR_INVALID_ARG, "q has %lld heads, not a multiple of the cache's %d", (long long)H, p.c.Hk);
+    if (m < 0 || m > 0x7ffffffe || H * (int64_t)p.c.B > 0x7fffffff || (H / p.c.Hk) * m > 0x7fffffff ||
+        H * (int64_t)p.c.B * m > (int64_t)1 << 36)
+        return fail(SPATTN_ERR_UNSUPPORTED, "q batch, heads or tokens too large");
+    if ((r = check_cache_rows(q, "q", p.c, H, m, d, q->dtype))) return r;
+    if ((r = check_cache_rows(out, "out", p.c, H, m, d, q->dtype))) return r;
+    if (!seqlen) return fail(SPATTN_ERR_INVALID_ARG, "seqlen is NULL");
+    if ((r = check_lens(seqlen, "seqlen"))) return r;
+    if ((r = check_lens(qlen, "qlen"))) return r;
+    if (n_global < 0) return fail(SPATTN_ERR_INVALID_ARG, "n_global < 0");
+    if (lse && ((uintptr_t)lse) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "lse not aligned");
+    if (!(scale == scale)) return fail(SPATTN_ERR_INVALID_ARG, "scale is NaN");
+    if ((int64_t)p.c.B * H * m == 0) return SPATTN_OK;
+    cudaStream_t s = (cudaStream_t)stream_v;
+    int dev;
+    CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
+    if ((r = err_flags_ptr(dev, &p.c.err))) return r;
+    auto bs = [](const spattn_tensor* t, int x) { return t->shape[x] == 1 ? 0 : t->stride[x]; };
+    p.q = q->data;
+    p.out = out->data;
+    p.lse = lse;
+    p.q_sb = bs(q, 0); p.q_sh = bs(q, 1); p.q_sn = bs(q, 2);
+    p.o_sb = bs(out, 0); p.o_sh = bs(out, 1); p.o_sn = bs(out, 2);
+    p.B = p.c.B;
+    p.H = (int)H;
+    p.G = (int)(H / p.c.Hk);
+    p.m = (int)m;
+    p.seqlen = seqlen;
+    p.qlen = qlen;
+    p.window = window;
+    p.n_global = n_global;
+    p.scale_log2 = scale * kLog2e;
+    const cudaError_t e = launch_fwd_cache(p, q->dtype == SPATTN_BF16 ? 0 : 1, code, d, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
+    return SPATTN_OK;
+}
+
 int spattn_check_device_error(void* stream_v) { return spattn_device_error(stream_v, nullptr); }
 
 int spattn_device_error(void* stream_v, uint32_t* flags) {
@@ -1912,6 +2089,8 @@ int spattn_device_error(void* stream_v, uint32_t* flags) {
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error flag");
     if (v & kErrTimeout) return fail(SPATTN_ERR_TIMEOUT, "a bounded wait in the tensor-core kernel expired");
     if (v & kErrBadColumn) return fail(SPATTN_ERR_BAD_CSR, "a column index outside [0, n) was skipped");
+    if (v & kErrBadPage) return fail(SPATTN_ERR_BAD_CACHE, "a cache call left out places that have no page");
+    if (v & kErrNonFinite) return fail(SPATTN_ERR_BAD_CACHE, "a NaN or an infinity was written to a cache");
     return SPATTN_OK;
 }
 
