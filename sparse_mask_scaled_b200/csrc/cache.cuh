@@ -89,9 +89,8 @@ struct CacheFwdParams {
     int n_global;
     float scale_log2;  // scale * log2(e)
 };
-constexpr int kCacheBlocksPerSm = 3;
 // Floats of workspace a call needs.
-int64_t fwd_cache_workspace(int d, int num_sms);
+int64_t fwd_cache_workspace(int real, int d, int num_sms);
 cudaError_t launch_fwd_cache(const CacheFwdParams& p, int real, int code, int d, int num_sms, float* ws,
                              cudaStream_t s);
 

@@ -6,12 +6,15 @@
 //     s_j = scale <q, k_j>,  out = sum_j softmax_j(s) v_j,  lse = log sum_j exp(s_j)
 //
 // Rows. The m * G rows (query t, head g of the group) of a (sequence, K/V head)
-// share its tokens and are cut into tiles of 16, the M of mma.m16n8k16 (fp16 in,
-// fp32 out). A row tile of one K/V head is a segment. Codes are exact in fp16,
-// and so are bf16 queries once a row is scaled by a power of two that brings its
-// largest element to [2^14, 2^15) (elements 2^-28 below it lose bits): QK^T is
-// exact up to fp32 accumulation. fp32 queries and their weights go in as the sum
-// of two fp16 numbers (22 bits), at twice the products.
+// share its tokens and are cut into tiles of 8 R rows, R = 1..4 as the rows need:
+// with tokens (then head dim elements) on the M side of mma.m16n8k16 and rows on
+// its N = 8 side, the common case of up to 8 rows wastes no products and holds O
+// in D / 4 registers, so that enough warps fit to keep HBM busy. A row tile of
+// one K/V head is a segment. Codes are exact in fp16, and so are bf16 queries
+// once a row is scaled by a power of two that brings its largest element to
+// [2^14, 2^15) (elements 2^-28 below it lose bits): K Q^T is exact up to fp32
+// accumulation. fp32 queries and their weights go in as the sum of two fp16
+// numbers (22 bits), at twice the products.
 //
 // Scales. A page's K scale multiplies its scores. Its V scale vs goes into the
 // exponent: p' = 2^(x + log2 vs - m) with x the score in base 2, so that weights
@@ -21,12 +24,12 @@
 // largest exponent - 5), so that most steps need no exchange between lanes.
 //
 // Streaming. The kernel is bound by HBM at long caches: each code is read once,
-// by cp.async of 16 (8, 4) bytes into a ring of kStages steps in shared memory.
+// by cp.async of 16 (8, 4) bytes into a ring of a few steps in shared memory.
 // A lane copies exactly the bytes that its own mma fragments need (any order of
 // d and of the output's columns does for a product as long as both sides use the
 // same one), so that nothing is exchanged, transposed or synchronised: K
 // fragments are 4 neighbouring codes of a token, V fragments byte columns of four
-// tokens. A warp's step is 128 / D sub-blocks of 16 tokens, each inside one page.
+// tokens. A warp's step is kSub sub-blocks of 16 tokens, each inside one page.
 //
 // Work. All segments' steps form one line, which the grid's blocks share evenly
 // (they know it from the lengths alone), so that one long sequence among short
@@ -43,7 +46,7 @@ namespace {
 
 using sm100::ex2;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr float kNone = -1e30f;      // reference of a row without a token so far
 constexpr float kRescaleAt = 12.f;   // largest exponent of a weight before the reference moves
 constexpr float kHeadroom = 5.f;     // exponent of the largest weight after it moved
@@ -58,11 +61,15 @@ struct Geo {
     static constexpr int kGroup = kWarps * kSub * 16; // tokens a block step
     static constexpr int kKBytes = D >= 64 ? 16 : 8;  // bytes a K copy
     static constexpr int kKCopies = D / (4 * kKBytes);// of each token, by a lane
-    static constexpr int kNT = D / 8;                 // mma tiles over the head dim = bytes a V copy
-    static constexpr int kSteps = D / 16;             // mma steps over the head dim
-    static constexpr int kStage = 4096;               // bytes of a warp's ring stage: K, then V
-    static constexpr int kPiece = 32 + 16 * D;        // floats of a stored piece
+    static constexpr int kVBytes = D / 8;             // bytes a V copy
+    static constexpr int kSteps = D / 16;             // mma steps over the head dim; mma tiles of O
+    static constexpr int kSide = kSub * 16 * D;       // bytes of K (and of V) in a warp's ring stage
 };
+// Floats of a stored piece: m and l of the 8 R rows, then O.
+template <int D, int R>
+constexpr int piece_floats() {
+    return 8 * R * (2 + D);
+}
 
 // A (sequence, row tile): the tokens its rows attend to, as groups of kGroup:
 // na groups of the global tokens [0, a_hi), then the groups from b_first on that
@@ -75,7 +82,7 @@ struct Tile {
     int full_hi, full_lo, full_a;  // every row attends to [full_lo, full_hi) of the second part, [0, full_a) of the first
 };
 
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ Tile make_tile(const CacheFwdParams& p, int b, int rt) {
     Tile t;
     const int64_t cap = cache_capacity(p.c);
@@ -84,9 +91,9 @@ __device__ __forceinline__ Tile make_tile(const CacheFwdParams& p, int b, int rt
     int nq = p.qlen ? p.qlen[b] : p.m;
     nq = nq < 0 ? 0 : nq < p.m ? nq : p.m;
     t.b = b;
-    t.first_row = rt * 16;
+    t.first_row = rt * 8 * R;
     const int64_t left = (int64_t)nq * p.G - t.first_row;
-    t.rows = (int)(left < 0 ? 0 : left < 16 ? left : 16);
+    t.rows = (int)(left < 0 ? 0 : left < 8 * R ? left : 8 * R);
     t.base = n - nq;
     const int lo_pos = t.base + t.first_row / p.G;
     const int hi_pos = t.base + (t.first_row + (t.rows > 0 ? t.rows : 1) - 1) / p.G;
@@ -106,7 +113,10 @@ __device__ __forceinline__ Tile make_tile(const CacheFwdParams& p, int b, int rt
     return t;
 }
 
-__host__ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p) { return (int)(((int64_t)p.m * p.G + 15) / 16); }
+template <int R>
+__host__ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p) {
+    return (int)(((int64_t)p.m * p.G + 8 * R - 1) / (8 * R));
+}
 
 // The line of all steps: entry e = (sequence, row tile) holds Hk segments one
 // after the other. Finds the total, and the entry that holds place `at` (in
@@ -115,13 +125,13 @@ __host__ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p) { ret
 struct Line {
     int64_t total;
 };
-template <int D>
-__device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[kWarps * 32 + 1]) {
-    const int entries = p.B * row_tiles(p), per = (entries + kWarps * 32 - 1) / (kWarps * 32);
+template <int D, int R>
+__device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[kThreads + 1]) {
+    const int entries = p.B * row_tiles<R>(p), per = (entries + kThreads - 1) / (kThreads);
     const int tid = threadIdx.x;
     int64_t mine = 0;
     for (int e = tid * per; e < entries && e < (tid + 1) * per; ++e)
-        mine += make_tile<D>(p, e / row_tiles(p), e % row_tiles(p)).groups;
+        mine += make_tile<D, R>(p, e / row_tiles<R>(p), e % row_tiles<R>(p)).groups;
     // inclusive scan over the block
     int64_t x = mine;
 #pragma unroll
@@ -137,14 +147,14 @@ __device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[kWarps * 32 
     __syncthreads();
     sums[tid + 1] = x + before;
     __syncthreads();
-    return Line{sums[kWarps * 32] * p.c.Hk};
+    return Line{sums[kThreads] * p.c.Hk};
 }
 // The entry that holds place `at` < total, and its first place.
-template <int D>
-__device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[kWarps * 32 + 1], int64_t at, int* entry,
+template <int D, int R>
+__device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[kThreads + 1], int64_t at, int* entry,
                           int64_t* first) {
-    const int per = (p.B * row_tiles(p) + kWarps * 32 - 1) / (kWarps * 32);
-    int lo = 0, hi = kWarps * 32 - 1;  // the thread whose entries hold it
+    const int per = (p.B * row_tiles<R>(p) + kThreads - 1) / (kThreads);
+    int lo = 0, hi = kThreads - 1;  // the thread whose entries hold it
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (sums[mid + 1] * p.c.Hk > at) hi = mid;
@@ -153,7 +163,7 @@ __device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[kWarps 
     int e = lo * per;
     int64_t place = sums[lo] * p.c.Hk;
     while (true) {
-        const int64_t len = (int64_t)make_tile<D>(p, e / row_tiles(p), e % row_tiles(p)).groups * p.c.Hk;
+        const int64_t len = (int64_t)make_tile<D, R>(p, e / row_tiles<R>(p), e % row_tiles<R>(p)).groups * p.c.Hk;
         if (place + len > at) break;
         place += len;
         ++e;
@@ -166,7 +176,14 @@ __device__ __forceinline__ int line_blocks(int64_t total, int grid) { return tot
 __device__ __forceinline__ int64_t line_start(int64_t total, int blocks, int x) { return total * x / blocks; }
 
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async_or_zero(uint32_t dst, const void* src, bool there) {
     const int bytes = there ? N : 0;  // 0: N zeros
     if constexpr (N == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -180,13 +197,20 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t addr, uint32_t* w) {
-    if constexpr (N == 16)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
-    else if constexpr (N == 8)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+    if constexpr (N == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (N == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
 }
 
 // Four codes of a word as two fp16 pairs. int8: 1024 + (c + 128) is the fp16
@@ -207,8 +231,7 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -224,183 +247,194 @@ __device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t h) {
     return half_pair(a - __low2float(v), b - __high2float(v));
 }
 
+// Transposes an 8 x 8 matrix of fp16 held as lane (g, c): row g, columns 2 c, 2 c + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // A tile's running state in one warp: lane (g = lane / 4, c = lane % 4) holds rows
-// g and g + 8. o[j][2 r + e] is row g + 8 r, element NT (2 c + e) + j; m and l
-// are the row's (l: this lane's part until it is summed over c).
-template <int D>
+// 8 k + 2 c + e. o[k][i][2 x + e] is element kVBytes g + 2 i + x of that row; l is
+// this lane's part of the row's sum until it is summed over g.
+template <int D, int R>
 struct State {
-    float o[Geo<D>::kNT][4];
-    float m[2], l[2];
+    float o[R][Geo<D>::kSteps][4];
+    float m[R][2], l[R][2];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int j = 0; j < Geo<D>::kNT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        m[0] = m[1] = kNone;
-        l[0] = l[1] = 0.f;
-    }
-    __device__ __forceinline__ void scale(float a0, float a1) {
+        for (int k = 0; k < R; ++k) {
 #pragma unroll
-        for (int j = 0; j < Geo<D>::kNT; ++j) {
-            o[j][0] *= a0;
-            o[j][1] *= a0;
-            o[j][2] *= a1;
-            o[j][3] *= a1;
+            for (int i = 0; i < Geo<D>::kSteps; ++i) o[k][i][0] = o[k][i][1] = o[k][i][2] = o[k][i][3] = 0.f;
+            m[k][0] = m[k][1] = kNone;
+            l[k][0] = l[k][1] = 0.f;
         }
-        l[0] *= a0;
-        l[1] *= a1;
+    }
+    __device__ __forceinline__ void scale(int k, float a0, float a1) {
+#pragma unroll
+        for (int i = 0; i < Geo<D>::kSteps; ++i) {
+            o[k][i][0] *= a0;
+            o[k][i][1] *= a1;
+            o[k][i][2] *= a0;
+            o[k][i][3] *= a1;
+        }
+        l[k][0] *= a0;
+        l[k][1] *= a1;
+    }
+    __device__ __forceinline__ float4 get(int k, int i) const { return make_float4(o[k][i][0], o[k][i][1], o[k][i][2], o[k][i][3]); }
+    __device__ __forceinline__ void add(int k, int i, const float4& v, float w0, float w1) {
+        o[k][i][0] += v.x * w0;
+        o[k][i][1] += v.y * w1;
+        o[k][i][2] += v.z * w0;
+        o[k][i][3] += v.w * w1;
     }
 };
 
-template <int D>
-struct Join {
-    float ml[kWarps][2][16];
-    float4 o[2][Geo<D>::kNT][32];  // lane-linear
+// Where the warps' states meet. o may lie over the ring: join_warps writes it
+// after a barrier.
+template <int D, int R>
+struct JoinO {
+    float4 o[2][R * Geo<D>::kSteps][32];
 };
-
-template <int D>
-__device__ __forceinline__ float4 get4(const State<D>& s, int x) {  // x: constant after unrolling
-    const int r = x / (Geo<D>::kNT / 2), e = x / (Geo<D>::kNT / 4) % 2, j = x % (Geo<D>::kNT / 4) * 4;
-    return make_float4(s.o[j][2 * r + e], s.o[j + 1][2 * r + e], s.o[j + 2][2 * r + e], s.o[j + 3][2 * r + e]);
-}
-template <int D>
-__device__ __forceinline__ void add4(State<D>& s, int x, const float4& v, float a) {
-    const int r = x / (Geo<D>::kNT / 2), e = x / (Geo<D>::kNT / 4) % 2, j = x % (Geo<D>::kNT / 4) * 4;
-    s.o[j][2 * r + e] += v.x * a;
-    s.o[j + 1][2 * r + e] += v.y * a;
-    s.o[j + 2][2 * r + e] += v.z * a;
-    s.o[j + 3][2 * r + e] += v.w * a;
-}
+template <int R>
+using JoinMl = float[kWarps][2][8 * R];
 
 // The block's warps' states (l summed over the row's lanes) joined into warp 0's.
-template <int D>
-__device__ __forceinline__ void join_warps(State<D>& s, Join<D>& sh) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    if ((lane & 3) == 0) {
-        sh.ml[warp][0][g] = s.m[0];
-        sh.ml[warp][0][g + 8] = s.m[1];
+template <int D, int R>
+__device__ __forceinline__ void join_warps(State<D, R>& s, JoinMl<R>& ml, JoinO<D, R>& sh) {
+    constexpr int N = Geo<D>::kSteps;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
+    if (lane < 4) {
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) ml[warp][0][8 * k + 2 * c + e] = s.m[k][e];
     }
     __syncthreads();
-    float top[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        top[r] = sh.ml[0][0][g + 8 * r];
+    for (int k = 0; k < R; ++k) {
+        float top[2];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top[r] = fmaxf(top[r], sh.ml[w][0][g + 8 * r]);
-    }
-    s.scale(ex2(s.m[0] - top[0]), ex2(s.m[1] - top[1]));
-    s.m[0] = top[0];
-    s.m[1] = top[1];
-    if ((lane & 3) == 0) {
-        sh.ml[warp][1][g] = s.l[0];
-        sh.ml[warp][1][g + 8] = s.l[1];
+        for (int e = 0; e < 2; ++e) {
+            const int row = 8 * k + 2 * c + e;
+            top[e] = ml[0][0][row];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top[e] = fmaxf(top[e], ml[w][0][row]);
+        }
+        s.scale(k, ex2(s.m[k][0] - top[0]), ex2(s.m[k][1] - top[1]));
+        s.m[k][0] = top[0];
+        s.m[k][1] = top[1];
+        if (lane < 4) {
+            ml[warp][1][8 * k + 2 * c] = s.l[k][0];
+            ml[warp][1][8 * k + 2 * c + 1] = s.l[k][1];
+        }
     }
     if (warp >= 2) {
 #pragma unroll
-        for (int x = 0; x < Geo<D>::kNT; ++x) sh.o[warp - 2][x][lane] = get4<D>(s, x);
+        for (int x = 0; x < R * N; ++x) sh.o[warp - 2][x][lane] = s.get(x / N, x % N);
     }
     __syncthreads();
     if (warp < 2) {
 #pragma unroll
-        for (int x = 0; x < Geo<D>::kNT; ++x) add4<D>(s, x, sh.o[warp][x][lane], 1.f);
-        if (warp == 1) {  // only this warp reads or wrote o[1] since the barrier
+        for (int x = 0; x < R * N; ++x) s.add(x / N, x % N, sh.o[warp][x][lane], 1.f, 1.f);
+        if (warp == 1) {  // each lane writes what only it has read
 #pragma unroll
-            for (int x = 0; x < Geo<D>::kNT; ++x) sh.o[1][x][lane] = get4<D>(s, x);
+            for (int x = 0; x < R * N; ++x) sh.o[1][x][lane] = s.get(x / N, x % N);
         }
     }
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
-        for (int x = 0; x < Geo<D>::kNT; ++x) add4<D>(s, x, sh.o[1][x][lane], 1.f);
+        for (int x = 0; x < R * N; ++x) s.add(x / N, x % N, sh.o[1][x][lane], 1.f, 1.f);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            s.l[r] = 0.f;
+        for (int k = 0; k < R; ++k)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s.l[r] += sh.ml[w][1][g + 8 * r];
-        }
+            for (int e = 0; e < 2; ++e) {
+                s.l[k][e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s.l[k][e] += ml[w][1][8 * k + 2 * c + e];
+            }
     }
     __syncthreads();  // the buffers may be written again
 }
 
 // Warp 0: the finished rows of a tile. Those behind the sequence's queries get
 // zeros: the state holds what a query of zeros gave.
-template <typename T, int D>
-__device__ __forceinline__ void write_rows(const CacheFwdParams& p, const Tile& tile, int hk, State<D>& s) {
+template <typename T, int D, int R>
+__device__ __forceinline__ void write_rows(const CacheFwdParams& p, const Tile& tile, int hk, const State<D, R>& s) {
+    constexpr int N = Geo<D>::kVBytes;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = tile.first_row + g + 8 * r;
-        if (row >= p.m * p.G) continue;
-        const int b = tile.b, t = row / p.G, h = hk * p.G + row % p.G;
-        if (g + 8 * r >= tile.rows) {
-            s.l[r] = 0.f;
+    for (int k = 0; k < R; ++k)
 #pragma unroll
-            for (int j = 0; j < Geo<D>::kNT; ++j) s.o[j][2 * r] = s.o[j][2 * r + 1] = 0.f;
-        }
-        const float l = s.l[r], inv = l != 0.f ? 1.f / l : 0.f;
-        T* out = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + t * p.o_sn + 2 * Geo<D>::kNT * c;
-        if constexpr (std::is_same<T, float>::value) {
+        for (int e = 0; e < 2; ++e) {
+            const int in_tile = 8 * k + 2 * c + e, row = tile.first_row + in_tile;
+            if (row >= p.m * p.G) continue;
+            const int b = tile.b, t = row / p.G, h = hk * p.G + row % p.G;
+            const bool there = in_tile < tile.rows && s.l[k][e] != 0.f;
+            const float inv = 1.f / s.l[k][e];
+            T* out = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + t * p.o_sn + N * g;
+            float v[N];
 #pragma unroll
-            for (int x = 0; x < Geo<D>::kNT / 2; ++x) {
-                const float4 v = get4<D>(s, r * (Geo<D>::kNT / 2) + x);
-                reinterpret_cast<float4*>(out)[x] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            }
-        } else {
+            for (int x = 0; x < N; ++x) v[x] = there ? s.o[k][x / 2][2 * (x & 1) + e] * inv : 0.f;
+            if constexpr (std::is_same<T, float>::value) {
 #pragma unroll
-            for (int x = 0; x < Geo<D>::kNT / 4; ++x) {
-                uint32_t u[4];
+                for (int x = 0; x < N; x += 4) *reinterpret_cast<float4*>(out + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            } else {
+                uint32_t u[N / 2];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float4 v = get4<D>(s, r * (Geo<D>::kNT / 2) + 2 * x + y);
-                    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * inv, v.y * inv),
-                                         d = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-                    u[2 * y] = *reinterpret_cast<const uint32_t*>(&a);
-                    u[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&d);
+                for (int x = 0; x < N / 2; ++x) {
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
+                    u[x] = *reinterpret_cast<const uint32_t*>(&a);
                 }
-                reinterpret_cast<uint4*>(out)[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                if constexpr (N >= 8) {
+#pragma unroll
+                    for (int x = 0; x < N / 2; x += 4) *reinterpret_cast<uint4*>(out + 2 * x) = make_uint4(u[x], u[x + 1], u[x + 2], u[x + 3]);
+                } else {
+                    *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
+                }
             }
+            if (p.lse && g == 0)
+                p.lse[((int64_t)b * p.H + h) * p.m + t] = there ? (s.m[k][e] + log2f(s.l[k][e])) * kLn2 : -INFINITY;
         }
-        if (p.lse && c == 0)
-            p.lse[((int64_t)b * p.H + h) * p.m + t] = l != 0.f ? (s.m[r] + log2f(l)) * kLn2 : -INFINITY;
-    }
 }
 
-// Pieces in the workspace: m and l of the 16 rows, then O lane-linear.
-template <int D>
-__device__ __forceinline__ void write_piece(float* ws, const State<D>& s, int rows) {
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+// Pieces in the workspace: m and l of the rows, then O by lane.
+template <int D, int R>
+__device__ __forceinline__ void write_piece(float* ws, const State<D, R>& s, int rows) {
+    constexpr int N = Geo<D>::kSteps;
+    const int lane = threadIdx.x & 31, c = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        if (g + 8 * r >= rows) continue;
-        if ((lane & 3) == 0) {
-            ws[g + 8 * r] = s.m[r];
-            ws[16 + g + 8 * r] = s.l[r];
+    for (int k = 0; k < R; ++k) {
+        const int row = 8 * k + 2 * c;
+        if (row >= rows) continue;
+        if (lane < 4) {
+            *reinterpret_cast<float2*>(ws + row) = make_float2(s.m[k][0], s.m[k][1]);
+            *reinterpret_cast<float2*>(ws + 8 * R + row) = make_float2(s.l[k][0], s.l[k][1]);
         }
 #pragma unroll
-        for (int x = 0; x < Geo<D>::kNT / 2; ++x)
-            reinterpret_cast<float4*>(ws + 32)[(r * (Geo<D>::kNT / 2) + x) * 32 + lane] =
-                get4<D>(s, r * (Geo<D>::kNT / 2) + x);
+        for (int i = 0; i < N; ++i) reinterpret_cast<float4*>(ws + 16 * R)[(k * N + i) * 32 + lane] = s.get(k, i);
     }
 }
 // Adds a piece to the state (whose l is complete in every lane of the row).
-template <int D>
-__device__ __forceinline__ void add_piece(const float* ws, State<D>& s, int rows) {
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+template <int D, int R>
+__device__ __forceinline__ void add_piece(const float* ws, State<D, R>& s, int rows) {
+    constexpr int N = Geo<D>::kSteps;
+    const int lane = threadIdx.x & 31, c = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        if (g + 8 * r >= rows) continue;
-        const float m = ws[g + 8 * r], l = ws[16 + g + 8 * r];
-        const float top = fmaxf(s.m[r], m), a = ex2(s.m[r] - top), w = ex2(m - top);
-        s.m[r] = top;
-        s.l[r] = s.l[r] * a + l * w;
+    for (int k = 0; k < R; ++k) {
+        const int row = 8 * k + 2 * c;
+        if (row >= rows) continue;
+        const float2 m = *reinterpret_cast<const float2*>(ws + row), l = *reinterpret_cast<const float2*>(ws + 8 * R + row);
+        const float top0 = fmaxf(s.m[k][0], m.x), top1 = fmaxf(s.m[k][1], m.y);
+        const float w0 = ex2(m.x - top0), w1 = ex2(m.y - top1);
+        s.scale(k, ex2(s.m[k][0] - top0), ex2(s.m[k][1] - top1));
+        s.m[k][0] = top0;
+        s.m[k][1] = top1;
+        s.l[k][0] += l.x * w0;
+        s.l[k][1] += l.y * w1;
 #pragma unroll
-        for (int j = 0; j < Geo<D>::kNT; ++j) {
-            s.o[j][2 * r] *= a;
-            s.o[j][2 * r + 1] *= a;
-        }
-#pragma unroll
-        for (int x = 0; x < Geo<D>::kNT / 2; ++x) {
-            const float4 v = reinterpret_cast<const float4*>(ws + 32)[(r * (Geo<D>::kNT / 2) + x) * 32 + lane];
-            add4<D>(s, r * (Geo<D>::kNT / 2) + x, v, w);
-        }
+        for (int i = 0; i < N; ++i) s.add(k, i, reinterpret_cast<const float4*>(ws + 16 * R)[(k * N + i) * 32 + lane], w0, w1);
     }
 }
 
@@ -409,39 +443,42 @@ template <typename T>
 constexpr int parts() {
     return std::is_same<T, float>::value ? 2 : 1;
 }
-template <typename T>
-constexpr int stages() {
-    return std::is_same<T, float>::value ? 4 : 3;
-}
-template <typename T>
-constexpr int blocks_per_sm() {  // registers: 168 a thread, or 255
-    return std::is_same<T, float>::value ? 2 : 3;
+constexpr int kStages = 3;  // of the ring
+// Blocks an SM holds (50 KB of shared memory each) with 128, 168 or 255 registers
+// a thread; O, Q and the scores take `held` of them.
+template <typename T, int D, int R>
+constexpr int blocks_per_sm() {
+    const int held = (D / 4 + parts<T>() * D / 8 + 4 * Geo<D>::kSub) * R;
+    return R == 1 ? 4 : held <= 104 ? 3 : 2;
 }
 
-template <typename T, int D>
+template <typename T, int D, int R>
 struct Shared {
-    uint8_t ring[kWarps][stages<T>()][Geo<D>::kStage];
-    float scales[kWarps][stages<T>()][2 * Geo<D>::kSub];  // K, V of each sub-block
-    Join<D> join;
-    int64_t sums[kWarps * 32 + 1];
+    union {
+        uint8_t ring[kWarps][kStages][2 * Geo<D>::kSide];  // a stage: K, then V
+        JoinO<D, R> join;
+    };
+    float scales[kWarps][kStages][2 * Geo<D>::kSub];  // K, V of each sub-block
+    JoinMl<R> ml;
+    int64_t sums[kThreads + 1];
 };
 
-// Queries of a tile as mma A fragments: row g + 8 r of step x holds the elements
-// that the lane's K bytes stand for.
-template <typename T, int D>
+// Queries of a tile as mma B fragments: column g of step x (rows 8 k + g) holds
+// the elements that the lane's K bytes stand for.
+template <typename T, int D, int R>
 struct Query {
-    uint32_t a[parts<T>()][Geo<D>::kSteps][4];
-    float factor[2];  // of a row's scores, to base 2
+    uint32_t b[parts<T>()][R][Geo<D>::kSteps][2];
+    float factor[R][2];  // of the scores of row 8 k + 2 c + e, to base 2
 };
-template <typename T, int D>
-__device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& t, int hk, Query<T, D>& q) {
+template <typename T, int D, int R>
+__device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& t, int hk, Query<T, D, R>& q) {
     using G = Geo<D>;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int k = 0; k < R; ++k) {
         float x[D / 4];
-        const int row = t.first_row + g + 8 * r;
-        if (g + 8 * r < t.rows) {
+        const int row = t.first_row + 8 * k + g;
+        if (8 * k + g < t.rows) {
             const T* src = static_cast<const T*>(p.q) + t.b * p.q_sb + (hk * p.G + row % p.G) * p.q_sh +
                            (row / p.G) * p.q_sn;
             constexpr int V = 16 / sizeof(T);
@@ -469,103 +506,124 @@ __device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& 
         int up = 0;  // 2^up brings the largest element to [2^14, 2^15)
         if (top > 0.f && top < INFINITY) up = 14 - ilogbf(top);
         up = up > 120 ? 120 : up;
-        const float by = exp2f((float)up);
-        q.factor[r] = p.scale_log2 * exp2f((float)-up);
+        const float by = exp2f((float)up), factor = p.scale_log2 * exp2f((float)-up);
+        q.factor[k][0] = __shfl_sync(0xffffffffu, factor, 8 * c);
+        q.factor[k][1] = __shfl_sync(0xffffffffu, factor, 8 * c + 4);
 #pragma unroll
-        for (int s = 0; s < G::kSteps; ++s) {
-            const float v0 = x[4 * s] * by, v1 = x[4 * s + 1] * by, v2 = x[4 * s + 2] * by, v3 = x[4 * s + 3] * by;
-            q.a[0][s][r] = half_pair(v0, v1);
-            q.a[0][s][2 + r] = half_pair(v2, v3);
-            if constexpr (parts<T>() == 2) {
-                q.a[1][s][r] = half_rest(v0, v1, q.a[0][s][r]);
-                q.a[1][s][2 + r] = half_rest(v2, v3, q.a[0][s][2 + r]);
+        for (int s = 0; s < G::kSteps; ++s)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float v0 = x[4 * s + 2 * y] * by, v1 = x[4 * s + 2 * y + 1] * by;
+                q.b[0][k][s][y] = half_pair(v0, v1);
+                if constexpr (parts<T>() == 2) q.b[1][k][s][y] = half_rest(v0, v1, q.b[0][k][s][y]);
             }
-        }
     }
 }
 
-// The first token of a warp's step in group x of the tile, and the run it belongs to.
+// A warp's walk over the groups of a tile: group x, its first token j.
 template <int D>
-__device__ __forceinline__ int step_tokens(const Tile& t, int x, int warp, int& lo, int& hi) {
-    const bool a = x < t.na;
-    lo = a ? 0 : t.b_lo;
-    hi = a ? t.a_hi : t.b_hi;
-    return (a ? x : t.b_first + x - t.na) * Geo<D>::kGroup + warp * Geo<D>::kSub * 16;
-}
+struct Walk {
+    int x, j;
+    __device__ __forceinline__ Walk(const Tile& t, int x0, int warp) : x(x0) {
+        j = (x0 < t.na ? x0 : t.b_first + x0 - t.na) * Geo<D>::kGroup + warp * Geo<D>::kSub * 16;
+    }
+    __device__ __forceinline__ void next(const Tile& t) {
+        ++x;
+        j = x == t.na ? j + (t.b_first - t.na + 1) * Geo<D>::kGroup : j + Geo<D>::kGroup;
+    }
+    __device__ __forceinline__ int lo(const Tile& t) const { return x < t.na ? 0 : t.b_lo; }
+    __device__ __forceinline__ int hi(const Tile& t) const { return x < t.na ? t.a_hi : t.b_hi; }
+};
 
-template <typename T, int CODE, int D>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T>()) k_fwd_cache(CacheFwdParams p, float* ws) {
+template <typename T, int CODE, int D, int R>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cache(CacheFwdParams p, float* ws) {
     using G = Geo<D>;
-    constexpr int kS = stages<T>(), kParts = parts<T>();
+    constexpr int kParts = parts<T>();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem_raw);
+    Shared<T, D, R>& sh = *reinterpret_cast<Shared<T, D, R>*>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const Line line = line_total<D>(p, sh.sums);
+    const Line line = line_total<D, R>(p, sh.sums);
     const int blocks = line_blocks(line.total, (int)gridDim.x);
     if ((int)blockIdx.x >= blocks) return;
     int64_t at = line_start(line.total, blocks, blockIdx.x);
     const int64_t end = line_start(line.total, blocks, blockIdx.x + 1);
     int entry;
     int64_t place;
-    line_find<D>(p, sh.sums, at, &entry, &place);
-    const int rts = row_tiles(p);
+    line_find<D, R>(p, sh.sums, at, &entry, &place);
+    const int rts = row_tiles<R>(p);
 
-    const uint32_t ring = sm100::smem_u32(&sh.ring[warp][0][0]) ;
-    const uint32_t scales = sm100::smem_u32(&sh.scales[warp][0][0]);
+    uint8_t* const ring = &sh.ring[warp][0][0];
+    const uint32_t ring_at = sm100::smem_u32(ring), scales_at = sm100::smem_u32(&sh.scales[warp][0][0]);
     const int page_mask = (1 << p.c.page_shift) - 1;
+    // this lane's bytes of a sub-block, from its first token
+    const uint32_t k_lane = (uint32_t)(g * p.c.k.s_t) + c * G::kKBytes, v_lane = (uint32_t)(2 * c * p.c.v.s_t) + g * G::kVBytes;
 
     while (at < end) {
-        const Tile t = make_tile<D>(p, entry / rts, entry % rts);
+        const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
         const int hk = (int)((at - place) / t.groups);
         const int first = (int)((at - place) % t.groups);
         const int last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past
-        Query<T, D> q;
-        load_query<T, D>(p, t, hk, q);
-        State<D> st;
+        Query<T, D, R> q;
+        load_query<T, D, R>(p, t, hk, q);
+        State<D, R> st;
         st.clear();
 
-        // the page of this lane's sub-block (lane % kSub) in group x, -1 where none is needed
-        auto page_of = [&](int x) -> int {
-            if (x >= last) return -1;
-            int lo, hi;
-            const int j = step_tokens<D>(t, x, warp, lo, hi) + 16 * (lane % G::kSub);
-            return j + 16 > lo && j < hi ? cache_page(p.c, t.b, j) : -1;
+        // the page of this lane's sub-block (lane % kSub) of a step, -1 where none is needed
+        auto page_of = [&](const Walk<D>& w) -> int {
+            const int j = w.j + 16 * (lane % G::kSub);
+            return w.x < last && j + 16 > w.lo(t) && j < w.hi(t) ? cache_page(p.c, t.b, j) : -1;
         };
-        auto issue = [&](int x, int my_page) {
-            if (x < last) {
-                const int stage = x % kS;
-                int lo, hi;
-                const int j0 = step_tokens<D>(t, x, warp, lo, hi);
-                const uint32_t kd = ring + stage * G::kStage, vd = kd + G::kStage / 2;
+        auto issue = [&](const Walk<D>& w, int my_page, int stage) {
+            if (w.x < last) {
+                const int lo = w.lo(t), hi = w.hi(t);
+                const uint32_t kd = ring_at + stage * 2 * G::kSide + lane * G::kKBytes;
+                const uint32_t vd = ring_at + stage * 2 * G::kSide + G::kSide + lane * G::kVBytes;
+                const bool whole = w.j >= lo && w.j + 16 * G::kSub <= hi && __all_sync(0xffffffffu, my_page >= 0);
 #pragma unroll
                 for (int sb = 0; sb < G::kSub; ++sb) {
                     const int pid = __shfl_sync(0xffffffffu, my_page, sb);
-                    const int j = j0 + 16 * sb;
-                    const uint8_t* kp = p.c.k.codes + (pid < 0 ? 0 : pid * p.c.k.s_p + hk * p.c.k.s_h + (j & page_mask) * p.c.k.s_t);
-                    const uint8_t* vp = p.c.v.codes + (pid < 0 ? 0 : pid * p.c.v.s_p + hk * p.c.v.s_h + (j & page_mask) * p.c.v.s_t);
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int o = 8 * nt + g;
-                        const bool there = pid >= 0 && j + o >= lo && j + o < hi;
-#pragma unroll
-                        for (int i = 0; i < G::kKCopies; ++i)
-                            copy_async<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes + lane * G::kKBytes,
-                                                   kp + (there ? o * p.c.k.s_t + (i * 4 + c) * G::kKBytes : 0), there);
+                    const int j = w.j + 16 * sb, place = j & page_mask;
+                    const uint8_t *kp = p.c.k.codes, *vp = p.c.v.codes;
+                    if (pid >= 0) {
+                        kp += pid * p.c.k.s_p + hk * p.c.k.s_h + place * p.c.k.s_t + k_lane;
+                        vp += pid * p.c.v.s_p + hk * p.c.v.s_h + place * p.c.v.s_t + v_lane;
                     }
+                    const uint32_t k8 = (uint32_t)(8 * p.c.k.s_t), v1 = (uint32_t)p.c.v.s_t, v8 = 8 * v1;
+                    if (whole) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int o = 2 * c + (r & 1) + 8 * (r >> 1);
-                        const bool there = pid >= 0 && j + o >= lo && j + o < hi;
-                        copy_async<G::kNT>(vd + (sb * 4 + r) * 32 * G::kNT + lane * G::kNT,
-                                           vp + (there ? o * p.c.v.s_t + g * G::kNT : 0), there);
+                        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                            for (int i = 0; i < G::kKCopies; ++i)
+                                copy_async<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes,
+                                                       kp + nt * k8 + i * 4 * G::kKBytes);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            copy_async<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes, vp + (r & 1) * v1 + (r >> 1) * v8);
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            const int o = j + 8 * nt + g;
+                            const bool there = pid >= 0 && o >= lo && o < hi;
+#pragma unroll
+                            for (int i = 0; i < G::kKCopies; ++i)
+                                copy_async_or_zero<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes,
+                                                               kp + (there ? nt * k8 + i * 4 * G::kKBytes : 0), there);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int o = j + 2 * c + (r & 1) + 8 * (r >> 1);
+                            const bool there = pid >= 0 && o >= lo && o < hi;
+                            copy_async_or_zero<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes,
+                                                       vp + (there ? (r & 1) * v1 + (r >> 1) * v8 : 0), there);
+                        }
                     }
                 }
                 if (lane < 2 * G::kSub) {  // lane: sub-block lane % kSub, of K or V
-                    const uint32_t dst = scales + (stage * 2 * G::kSub + lane) * 4;
+                    const uint32_t dst = scales_at + (stage * 2 * G::kSub + lane) * 4;
                     if (my_page >= 0)
-                        copy_async<4>(dst, (lane < G::kSub ? p.c.k.scale : p.c.v.scale) + (int64_t)my_page * p.c.Hk + hk, true);
+                        copy_async<4>(dst, (lane < G::kSub ? p.c.k.scale : p.c.v.scale) + (int64_t)my_page * p.c.Hk + hk);
                     else
                         asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(kNoPage) : "memory");
                 }
@@ -573,154 +631,189 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T>()) k_fwd_cache(C
             copy_commit();
         };
 
-        int page = page_of(first);
+        Walk<D> ahead(t, first, warp), now(t, first, warp);
+        int page = page_of(ahead), fill = 0, stage = 0;
 #pragma unroll
-        for (int s = 0; s < kS - 1; ++s) {
-            issue(first + s, page);
-            page = page_of(first + s + 1);
+        for (int s = 0; s < kStages - 1; ++s) {
+            issue(ahead, page, fill++);
+            ahead.next(t);
+            page = page_of(ahead);
         }
-        for (int x = first; x < last; ++x) {
-            copy_wait<kS - 2>();
+        for (; now.x < last; now.next(t)) {
+            copy_wait<kStages - 2>();
             __syncwarp();  // the other lanes' scales are there, and every lane is done with the stage refilled next
-            issue(x + kS - 1, page);
-            page = page_of(x + kS);
-            const int stage = x % kS;
-            int lo, hi;
-            const int j0 = step_tokens<D>(t, x, warp, lo, hi);
-            const uint32_t kd = ring + stage * G::kStage, vd = kd + G::kStage / 2;
+            issue(ahead, page, fill);
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+            ahead.next(t);
+            page = page_of(ahead);
+            const int lo = now.lo(t), hi = now.hi(t);
+            const uint8_t* kd = ring + stage * 2 * G::kSide + lane * G::kKBytes;
+            const uint8_t* vd = ring + stage * 2 * G::kSide + G::kSide + lane * G::kVBytes;
+            const float* sc = &sh.scales[warp][stage][0];
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (now.j + 16 * G::kSub <= lo || now.j >= hi) continue;
+            // S^T = K Q^T: e[k][sb][2 x + y]: row 8 k + 2 c + y, token 16 sb + 8 x + g
+            float e[R][G::kSub][4];
+            auto scores = [&]() {
 #pragma unroll
-            for (int sb = 0; sb < G::kSub; ++sb) {
-                const int j = j0 + 16 * sb;
-                if (j + 16 <= lo || j >= hi) continue;
-                float ks, vs;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(scales + (stage * 2 * G::kSub + sb) * 4) : "memory");
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(scales + (stage * 2 * G::kSub + G::kSub + sb) * 4) : "memory");
-                if (ks == kNoPage) continue;
-                const bool no_v = vs < kMinScale;
-                const float lv = no_v ? 0.f : log2f(vs), inv_vs = no_v ? 1.f : 1.f / vs;
-                // S = Q K^T
-                float s[2][4];
+                for (int sb = 0; sb < G::kSub; ++sb) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                    for (int k = 0; k < R; ++k) e[k][sb][0] = e[k][sb][1] = e[k][sb][2] = e[k][sb][3] = 0.f;
 #pragma unroll
                     for (int i = 0; i < G::kKCopies; ++i) {
-                        uint32_t w[G::kKBytes / 4];
-                        load_words<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes + lane * G::kKBytes, w);
+                        uint32_t w[2][G::kKBytes / 4];
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+                            load_words<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes, w[nt]);
 #pragma unroll
                         for (int y = 0; y < G::kKBytes / 4; ++y) {
-                            uint32_t b0, b1;
-                            codes_to_half<CODE>(w[y], b0, b1);
+                            uint32_t a[4];
+                            codes_to_half<CODE>(w[0][y], a[0], a[2]);
+                            codes_to_half<CODE>(w[1][y], a[1], a[3]);
 #pragma unroll
-                            for (int a = 0; a < kParts; ++a) mma_f16(s[nt], q.a[a][i * (G::kKBytes / 4) + y], b0, b1);
-                        }
-                    }
-                }
-                // exponents x + log2 vs - m, -inf where the row does not attend
-                const bool first_part = x < t.na;
-                const bool full = first_part ? j + 16 <= t.full_a
-                                             : j + 16 <= t.full_hi && (j >= t.full_lo || j + 16 <= t.full_a);
-                const float f0 = ks * q.factor[0], f1 = ks * q.factor[1];
-                float e[2][4];
-                auto exponents = [&](float m0, float m1) {
-                    const float a0 = lv - m0, a1 = lv - m1;
+                            for (int k = 0; k < R; ++k)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        e[nt][0] = fmaf(s[nt][0], f0, a0);
-                        e[nt][1] = fmaf(s[nt][1], f0, a0);
-                        e[nt][2] = fmaf(s[nt][2], f1, a1);
-                        e[nt][3] = fmaf(s[nt][3], f1, a1);
-                    }
-                    if (!full) {
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int row = g + 8 * r;
-                            const int pos = row < t.rows ? t.base + (t.first_row + row) / p.G : -1;
-#pragma unroll
-                            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const int tok = j + 8 * nt + 2 * c + y;
-                                    const bool sees = tok <= pos && tok >= lo && tok < hi &&
-                                                      (p.window < 0 || tok >= pos - p.window || tok < p.n_global);
-                                    if (!sees) e[nt][2 * r + y] = -INFINITY;
+                                for (int z = 0; z < kParts; ++z) {
+                                    const uint32_t(&b)[2] = q.b[z][k][i * (G::kKBytes / 4) + y];
+                                    mma_f16(e[k][sb], a, b[0], b[1]);
                                 }
                         }
                     }
-                };
-                auto top_of = [&](int r) {
-                    return fmaxf(fmaxf(e[0][2 * r], e[0][2 * r + 1]), fmaxf(e[1][2 * r], e[1][2 * r + 1]));
-                };
-                exponents(st.m[0], st.m[1]);
-                if (__any_sync(0xffffffffu, fmaxf(top_of(0), top_of(1)) > kRescaleAt)) {
-                    exponents(0.f, 0.f);
+                }
+            };
+            scores();
+            // to exponents x + log2 vs - m, -inf where a row does not attend
+            bool odd = false;  // a sub-block without a page or with a V scale of 0
+            float ks[G::kSub], lv[G::kSub], inv_vs[G::kSub];
+#pragma unroll
+            for (int sb = 0; sb < G::kSub; ++sb) {
+                const float vs = sc[G::kSub + sb];
+                ks[sb] = sc[sb];
+                odd |= vs < kMinScale;
+                lv[sb] = vs < kMinScale ? 0.f : sm100::lg2(vs);
+                inv_vs[sb] = vs < kMinScale ? 1.f : __frcp_rn(vs);
+            }
+            const bool in_a = now.x < t.na;
+            const int j_end = now.j + 16 * G::kSub;
+            const bool full = !odd && (in_a ? j_end <= t.full_a
+                                            : j_end <= t.full_hi && (now.j >= t.full_lo || j_end <= t.full_a));
+            auto exponents = [&](bool from_zero) {
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int sb = 0; sb < G::kSub; ++sb)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float f = ks[sb] * q.factor[k][y], a = from_zero ? lv[sb] : lv[sb] - st.m[k][y];
+                            e[k][sb][y] = fmaf(e[k][sb][y], f, a);
+                            e[k][sb][2 + y] = fmaf(e[k][sb][2 + y], f, a);
+                        }
+                if (!full) {
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int row = 8 * k + 2 * c + y;
+                            const int pos = row < t.rows ? t.base + (t.first_row + row) / p.G : -1;
+#pragma unroll
+                            for (int sb = 0; sb < G::kSub; ++sb)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const int tok = now.j + 16 * sb + 8 * x + g;
+                                    const bool sees = tok <= pos && tok >= lo && tok < hi && ks[sb] != kNoPage &&
+                                                      (p.window < 0 || tok >= pos - p.window || tok < p.n_global);
+                                    if (!sees) e[k][sb][2 * x + y] = -INFINITY;
+                                }
+                        }
+                }
+            };
+            auto top_of = [&](int k, int y) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int sb = 0; sb < G::kSub; ++sb) top = sm100::fmax3(top, e[k][sb][y], e[k][sb][2 + y]);
+                return top;
+            };
+            exponents(false);
+            float most = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < R; ++k) most = sm100::fmax3(most, top_of(k, 0), top_of(k, 1));
+            if (__any_sync(0xffffffffu, most > kRescaleAt)) {
+                scores();  // again: the exponents took their place
+                exponents(true);
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
                     float m[2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float top = top_of(r);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        m[r] = top - st.m[r] > kRescaleAt ? top - kHeadroom : st.m[r];
+                    for (int y = 0; y < 2; ++y) {
+                        float top = top_of(k, y);
+#pragma unroll
+                        for (int z = 4; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+                        m[y] = top - st.m[k][y] > kRescaleAt ? top - kHeadroom : st.m[k][y];
                     }
-                    st.scale(ex2(st.m[0] - m[0]), ex2(st.m[1] - m[1]));
-                    st.m[0] = m[0];
-                    st.m[1] = m[1];
-                    exponents(m[0], m[1]);
+                    st.scale(k, ex2(st.m[k][0] - m[0]), ex2(st.m[k][1] - m[1]));
+                    st.m[k][0] = m[0];
+                    st.m[k][1] = m[1];
+#pragma unroll
+                    for (int sb = 0; sb < G::kSub; ++sb)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) e[k][sb][y] -= m[y & 1];
                 }
-                float sum0 = 0.f, sum1 = 0.f;
+            }
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+            for (int k = 0; k < R; ++k)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) e[nt][y] = ex2(e[nt][y]);
-                    sum0 += e[nt][0] + e[nt][1];
-                    sum1 += e[nt][2] + e[nt][3];
+                for (int sb = 0; sb < G::kSub; ++sb) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) e[k][sb][y] = ex2(e[k][sb][y]);
+                    st.l[k][0] = fmaf(e[k][sb][0] + e[k][sb][2], inv_vs[sb], st.l[k][0]);
+                    st.l[k][1] = fmaf(e[k][sb][1] + e[k][sb][3], inv_vs[sb], st.l[k][1]);
                 }
-                st.l[0] = fmaf(sum0, inv_vs, st.l[0]);
-                st.l[1] = fmaf(sum1, inv_vs, st.l[1]);
-                if (no_v) continue;
-                // O += P V
-                uint32_t pa[kParts][4];
+            // O^T += V^T P^T
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+            for (int sb = 0; sb < G::kSub; ++sb) {
+                if (odd && sc[G::kSub + sb] < kMinScale) continue;
+                uint32_t pb[kParts][R][2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        pa[0][2 * nt + r] = half_pair(e[nt][2 * r], e[nt][2 * r + 1]);
-                        if constexpr (kParts == 2)
-                            pa[1][2 * nt + r] = half_rest(e[nt][2 * r], e[nt][2 * r + 1], pa[0][2 * nt + r]);
+                for (int k = 0; k < R; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float p0 = e[k][sb][2 * x], p1 = e[k][sb][2 * x + 1];
+                        const uint32_t h = half_pair(p0, p1);
+                        pb[0][k][x] = transpose8(h);
+                        if constexpr (kParts == 2) pb[1][k][x] = transpose8(half_rest(p0, p1, h));
                     }
-                uint32_t v[4][(G::kNT + 3) / 4];
+                uint32_t v[4][(G::kVBytes + 3) / 4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) load_words<G::kNT>(vd + (sb * 4 + r) * 32 * G::kNT + lane * G::kNT, v[r]);
+                for (int r = 0; r < 4; ++r) load_words<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes, v[r]);
 #pragma unroll
-                for (int y = 0; y < G::kNT / 4; ++y) {
+                for (int y = 0; y < G::kVBytes / 4; ++y)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {  // byte columns 4 y + 2 z, + 1
                         const unsigned pick = z ? 0x7362 : 0x5140;
-                        uint32_t b[2][2];
-                        codes_to_half<CODE>(__byte_perm(v[0][y], v[1][y], pick), b[0][0], b[1][0]);
-                        codes_to_half<CODE>(__byte_perm(v[2][y], v[3][y], pick), b[0][1], b[1][1]);
+                        uint32_t a[4];
+                        codes_to_half<CODE>(__byte_perm(v[0][y], v[1][y], pick), a[0], a[1]);
+                        codes_to_half<CODE>(__byte_perm(v[2][y], v[3][y], pick), a[2], a[3]);
 #pragma unroll
-                        for (int a = 0; a < kParts; ++a) {
-                            mma_f16(st.o[4 * y + 2 * z], pa[a], b[0][0], b[0][1]);
-                            mma_f16(st.o[4 * y + 2 * z + 1], pa[a], b[1][0], b[1][1]);
-                        }
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int w = 0; w < kParts; ++w) mma_f16(st.o[k][2 * y + z], a, pb[w][k][0], pb[w][k][1]);
                     }
-                }
             }
         }
         copy_wait<0>();
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
-        }
-        join_warps<D>(st, sh.join);
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int z = 4; z < 32; z <<= 1) st.l[k][e] += __shfl_xor_sync(0xffffffffu, st.l[k][e], z);
+        join_warps<D, R>(st, sh.ml, sh.join);
         if (warp == 0) {
             if (first == 0 && last == t.groups)
-                write_rows<T, D>(p, t, hk, st);
+                write_rows<T, D, R>(p, t, hk, st);
             else  // slot 0: a segment that an earlier block began; slot 1: one that a later block goes on with
-                write_piece<D>(ws + ((int64_t)blockIdx.x * 2 + (first == 0)) * G::kPiece, st, t.rows);
+                write_piece<D, R>(ws + ((int64_t)blockIdx.x * 2 + (first == 0)) * piece_floats<D, R>(), st, t.rows);
         }
         at += last - first;
         if (at >= place + (int64_t)t.groups * p.c.Hk) {
@@ -732,18 +825,19 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<T>()) k_fwd_cache(C
 
 // Block x: segment x (entry x / Hk). The pieces of a segment that several blocks
 // worked on are added up, each warp taking every fourth.
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
-    __shared__ Join<D> join;
-    __shared__ int64_t sums[kWarps * 32 + 1];
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
+    __shared__ JoinO<D, R> join;
+    __shared__ JoinMl<R> ml;
+    __shared__ int64_t sums[kThreads + 1];
     const int warp = threadIdx.x >> 5;
-    const Line line = line_total<D>(p, sums);
-    const int blocks = line_blocks(line.total, grid), rts = row_tiles(p);
+    const Line line = line_total<D, R>(p, sums);
+    const int blocks = line_blocks(line.total, grid), rts = row_tiles<R>(p);
     const int entry = blockIdx.x / p.c.Hk, hk = blockIdx.x % p.c.Hk;
-    const int per = (p.B * rts + kWarps * 32 - 1) / (kWarps * 32);
+    const int per = (p.B * rts + kThreads - 1) / (kThreads);
     int64_t place = sums[entry / per];
-    for (int e = entry / per * per; e < entry; ++e) place += make_tile<D>(p, e / rts, e % rts).groups;
-    const Tile t = make_tile<D>(p, entry / rts, entry % rts);
+    for (int e = entry / per * per; e < entry; ++e) place += make_tile<D, R>(p, e / rts, e % rts).groups;
+    const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
     const int64_t s0 = place * p.c.Hk + (int64_t)hk * t.groups, s1 = s0 + t.groups - 1;
     // the block that holds place s: the last x with total x / blocks <= s
     auto block_of = [&](int64_t s) {
@@ -755,33 +849,45 @@ __global__ void __launch_bounds__(kWarps * 32) k_fwd_cache_join(CacheFwdParams p
     const int x0 = block_of(s0), x1 = block_of(s1);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // every block, so that this kernel ends after the first
     if (x0 == x1) return;
-    State<D> st;
+    State<D, R> st;
     st.clear();
     for (int x = x0 + warp; x <= x1; x += kWarps)
-        add_piece<D>(ws + ((int64_t)x * 2 + (x == x0)) * Geo<D>::kPiece, st, t.rows);
-    join_warps<D>(st, join);
-    if (warp == 0) write_rows<T, D>(p, t, hk, st);
+        add_piece<D, R>(ws + ((int64_t)x * 2 + (x == x0)) * piece_floats<D, R>(), st, t.rows);
+    join_warps<D, R>(st, ml, join);
+    if (warp == 0) write_rows<T, D, R>(p, t, hk, st);
 }
 
-template <typename T, int CODE, int D>
-cudaError_t fwd_d(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t s) {
-    const int smem = (int)sizeof(Shared<T, D>);
-    cudaError_t e = cudaFuncSetAttribute(k_fwd_cache<T, CODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int CODE, int D, int R>
+cudaError_t fwd_r(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t s) {
+    const int smem = (int)sizeof(Shared<T, D, R>);
+    cudaError_t e = cudaFuncSetAttribute(k_fwd_cache<T, CODE, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int grid = num_sms * kCacheBlocksPerSm;
-    const int use = grid / kCacheBlocksPerSm * blocks_per_sm<T>();
-    k_fwd_cache<T, CODE, D><<<use, kWarps * 32, smem, counted(s)>>>(p, ws);
+    const int grid = num_sms * blocks_per_sm<T, D, R>();
+    k_fwd_cache<T, CODE, D, R><<<grid, kThreads, smem, counted(s)>>>(p, ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.B * row_tiles(p) * p.c.Hk));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.gridDim = dim3((unsigned)((int64_t)p.B * row_tiles<R>(p) * p.c.Hk));
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = counted(s);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_fwd_cache_join<T, D>, p, (const float*)ws, use);
+    return cudaLaunchKernelEx(&cfg, k_fwd_cache_join<T, D, R>, p, (const float*)ws, grid);
+}
+
+// R as the rows need: each further 8 rows cost products but no bytes.
+template <typename T, int CODE, int D>
+cudaError_t fwd_d(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t s) {
+    const int rows = p.m * p.G;
+    if (rows <= 8) return fwd_r<T, CODE, D, 1>(p, num_sms, ws, s);
+    if (rows <= 16 || parts<T>() == 2) return fwd_r<T, CODE, D, 2>(p, num_sms, ws, s);
+    if constexpr (parts<T>() == 1) {
+        if (rows <= 24) return fwd_r<T, CODE, D, 3>(p, num_sms, ws, s);
+        return fwd_r<T, CODE, D, 4>(p, num_sms, ws, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <typename T, int CODE>
@@ -793,9 +899,25 @@ cudaError_t fwd_code(const CacheFwdParams& p, int d, int num_sms, float* ws, cud
     }
 }
 
+template <typename T, int D>
+constexpr int64_t workspace_per_sm() {  // two pieces a block
+    int64_t most = 0;
+    const int64_t r1 = 2 * blocks_per_sm<T, D, 1>() * piece_floats<D, 1>(), r2 = 2 * blocks_per_sm<T, D, 2>() * piece_floats<D, 2>(),
+                  r3 = 2 * blocks_per_sm<T, D, 3>() * piece_floats<D, 3>(), r4 = 2 * blocks_per_sm<T, D, 4>() * piece_floats<D, 4>();
+    most = r1 > r2 ? r1 : r2;
+    most = most > r3 ? most : r3;
+    return most > r4 ? most : r4;
+}
+
 }  // namespace
 
-int64_t fwd_cache_workspace(int d, int num_sms) { return (int64_t)num_sms * kCacheBlocksPerSm * 2 * (32 + 16 * d); }
+int64_t fwd_cache_workspace(int real, int d, int num_sms) {
+    if (real == 0)
+        return num_sms * (d == 32 ? workspace_per_sm<__nv_bfloat16, 32>() : d == 64 ? workspace_per_sm<__nv_bfloat16, 64>()
+                                                                                    : workspace_per_sm<__nv_bfloat16, 128>());
+    return num_sms * (d == 32 ? workspace_per_sm<float, 32>() : d == 64 ? workspace_per_sm<float, 64>()
+                                                                        : workspace_per_sm<float, 128>());
+}
 
 cudaError_t launch_fwd_cache(const CacheFwdParams& p, int real, int code, int d, int num_sms, float* ws,
                              cudaStream_t s) {

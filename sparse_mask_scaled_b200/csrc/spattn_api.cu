@@ -2044,7 +2044,7 @@ int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const in
     if (H < 1 || H % p.c.Hk != 0)
         return fail(SPATTN_ERR_INVALID_ARG, "q has %lld heads, not a multiple of the cache's %d", (long long)H, p.c.Hk);
     if (m < 0 || m > 0x7ffffffe || H * (int64_t)p.c.B > 0x7fffffff || (H / p.c.Hk) * m > 0x7ffffff0 ||
-        (int64_t)p.c.B * p.c.Hk * (((H / p.c.Hk) * m + 15) / 16) > 0x7fffffff)
+        (int64_t)p.c.B * p.c.Hk * (((H / p.c.Hk) * m + 7) / 8) > 0x7fffffff)
         return fail(SPATTN_ERR_UNSUPPORTED, "q batch, heads or tokens too large");
     if ((r = check_cache_rows(q, "q", p.c, H, m, d, q->dtype))) return r;
     if ((r = check_cache_rows(out, "out", p.c, H, m, d, q->dtype))) return r;
@@ -2077,9 +2077,10 @@ int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const in
     cudaMemPool_t pool;
     int sms;
     CUDA_TRY(device_state(dev, &pool, &sms), "memory pool");
+    const int real = q->dtype == SPATTN_BF16 ? 0 : 1;
     float* ws = nullptr;
-    CUDA_TRY(pool_alloc(&ws, fwd_cache_workspace(d, sms), pool, s), "cache attention workspace");
-    const cudaError_t e = launch_fwd_cache(p, q->dtype == SPATTN_BF16 ? 0 : 1, code, d, sms, ws, s);
+    CUDA_TRY(pool_alloc(&ws, fwd_cache_workspace(real, d, sms), pool, s), "cache attention workspace");
+    const cudaError_t e = launch_fwd_cache(p, real, code, d, sms, ws, s);
     const cudaError_t ef = cudaFreeAsync(ws, s);
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
     if (ef != cudaSuccess) return cuda_fail(ef, "cudaFreeAsync");
