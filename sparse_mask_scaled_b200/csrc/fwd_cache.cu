@@ -23,13 +23,15 @@
 // reference that moves only when some p' would pass 2^12 (it then becomes the
 // largest exponent - 5), so that most steps need no exchange between lanes.
 //
-// Streaming. The kernel is bound by HBM at long caches: each code is read once,
-// by cp.async of 16 (8, 4) bytes into a ring of a few steps in shared memory.
-// A lane copies exactly the bytes that its own mma fragments need (any order of
-// d and of the output's columns does for a product as long as both sides use the
-// same one), so that nothing is exchanged, transposed or synchronised: K
-// fragments are 4 neighbouring codes of a token, V fragments byte columns of four
-// tokens. A warp's step is kSub sub-blocks of 16 tokens, each inside one page.
+// Streaming. The kernel is bound by HBM at long caches: each code is read once.
+// Each warp has a ring of its own in shared memory, filled by TMA: a copy brings
+// 16 tokens of one page (4-D map {d, token, head, page}, any strides), swizzled so
+// that the fragment loads meet few bank conflicts. A step is kSub such sub-blocks
+// of K and of V. Fragments need no exchange between lanes: any order of the head
+// dim and of the tokens does for a product as long as both sides use the same, so
+// K fragments are 4 neighbouring codes of a token, and V fragments byte columns of
+// four tokens. The page table's entry and the page's scales are read a step
+// before they are used.
 //
 // Work. All segments' steps form one line, which the grid's blocks share evenly
 // (they know it from the lengths alone), so that one long sequence among short
@@ -39,6 +41,7 @@
 #include "cache.cuh"
 #include "sm100_ptx.cuh"
 
+#include <mutex>
 #include <type_traits>
 
 namespace spattn {
@@ -52,6 +55,8 @@ constexpr float kRescaleAt = 12.f;   // largest exponent of a weight before the 
 constexpr float kHeadroom = 5.f;     // exponent of the largest weight after it moved
 constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: a V scale below it counts as 0
 
+constexpr long long kCacheWaitCycles = 2000000000LL;  // limit of a wait for a copy: about one second
+constexpr int kUnread = -0x7fffffff; // page of a sub-block that needs none
 constexpr float kNoPage = -1.f;      // in place of the K scale of a sub-block that has no page
 
 // Sizes that follow from the head dim.
@@ -59,11 +64,20 @@ template <int D>
 struct Geo {
     static constexpr int kSub = 128 / D;              // sub-blocks of 16 tokens a warp step
     static constexpr int kGroup = kWarps * kSub * 16; // tokens a block step
-    static constexpr int kKBytes = D >= 64 ? 16 : 8;  // bytes a K copy
-    static constexpr int kKCopies = D / (4 * kKBytes);// of each token, by a lane
-    static constexpr int kVBytes = D / 8;             // bytes a V copy
+    static constexpr int kKBytes = D >= 64 ? 16 : 8;  // bytes of a K load
+    static constexpr int kKLoads = D / (4 * kKBytes); // of each token, by a lane
+    static constexpr int kVBytes = D / 8;             // bytes of a V load
     static constexpr int kSteps = D / 16;             // mma steps over the head dim; mma tiles of O
-    static constexpr int kSide = kSub * 16 * D;       // bytes of K (and of V) in a warp's ring stage
+    static constexpr int kBox = 16 * D;               // bytes of a sub-block of K or V
+    static constexpr int kSide = kSub * kBox;         // bytes of K (and of V) in a ring stage
+    // The token of a sub-block's half that stands at row x of a product (D = 128:
+    // neighbours differ in bit 2, so that the swizzle spreads their loads).
+    static __device__ __forceinline__ int token(int x) { return D == 128 ? (0x37156240 >> (4 * x)) & 7 : x; }
+    // Byte `at` of token o's row in a sub-block: the copy's swizzle exchanges 16-byte units.
+    static __device__ __forceinline__ int byte(int o, int at) {
+        const int x = D == 128 ? o & 7 : D == 64 ? (o >> 1) & 3 : (o >> 2) & 1;
+        return o * D + (at ^ (16 * x));
+    }
 };
 // Floats of a stored piece: m and l of the 8 R rows, then O.
 template <int D, int R>
@@ -176,27 +190,6 @@ __device__ __forceinline__ int line_blocks(int64_t total, int grid) { return tot
 __device__ __forceinline__ int64_t line_start(int64_t total, int blocks, int x) { return total * x / blocks; }
 
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void copy_async_or_zero(uint32_t dst, const void* src, bool there) {
-    const int bytes = there ? N : 0;  // 0: N zeros
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
     if constexpr (N == 16) {
         const uint4 v = *reinterpret_cast<const uint4*>(p);
@@ -291,7 +284,7 @@ struct State {
 };
 
 // Where the warps' states meet. o may lie over the ring: join_warps writes it
-// after a barrier.
+// after a barrier, and makes the writes known to the copies that refill it.
 template <int D, int R>
 struct JoinO {
     float4 o[2][R * Geo<D>::kSteps][32];
@@ -355,6 +348,7 @@ __device__ __forceinline__ void join_warps(State<D, R>& s, JoinMl<R>& ml, JoinO<
                 for (int w = 0; w < kWarps; ++w) s.l[k][e] += ml[w][1][8 * k + 2 * c + e];
             }
     }
+    sm100::fence_proxy_async_smem();
     __syncthreads();  // the buffers may be written again
 }
 
@@ -416,28 +410,6 @@ __device__ __forceinline__ void write_piece(float* ws, const State<D, R>& s, int
         for (int i = 0; i < N; ++i) reinterpret_cast<float4*>(ws + 16 * R)[(k * N + i) * 32 + lane] = s.get(k, i);
     }
 }
-// Adds a piece to the state (whose l is complete in every lane of the row).
-template <int D, int R>
-__device__ __forceinline__ void add_piece(const float* ws, State<D, R>& s, int rows) {
-    constexpr int N = Geo<D>::kSteps;
-    const int lane = threadIdx.x & 31, c = lane & 3;
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-        const int row = 8 * k + 2 * c;
-        if (row >= rows) continue;
-        const float2 m = *reinterpret_cast<const float2*>(ws + row), l = *reinterpret_cast<const float2*>(ws + 8 * R + row);
-        const float top0 = fmaxf(s.m[k][0], m.x), top1 = fmaxf(s.m[k][1], m.y);
-        const float w0 = ex2(m.x - top0), w1 = ex2(m.y - top1);
-        s.scale(k, ex2(s.m[k][0] - top0), ex2(s.m[k][1] - top1));
-        s.m[k][0] = top0;
-        s.m[k][1] = top1;
-        s.l[k][0] += l.x * w0;
-        s.l[k][1] += l.y * w1;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s.add(k, i, reinterpret_cast<const float4*>(ws + 16 * R)[(k * N + i) * 32 + lane], w0, w1);
-    }
-}
-
 // fp32: two fp16 parts.
 template <typename T>
 constexpr int parts() {
@@ -452,16 +424,18 @@ constexpr int blocks_per_sm() {
     return R == 1 ? 4 : held <= 104 ? 3 : 2;
 }
 
-template <typename T, int D, int R>
+template <int D, int R>
 struct Shared {
     union {
         uint8_t ring[kWarps][kStages][2 * Geo<D>::kSide];  // a stage: K, then V
         JoinO<D, R> join;
     };
     float scales[kWarps][kStages][2 * Geo<D>::kSub];  // K, V of each sub-block
+    uint64_t full[kWarps][kStages];
     JoinMl<R> ml;
     int64_t sums[kThreads + 1];
 };
+constexpr int kRingAlign = 1024;  // the swizzle's period
 
 // Queries of a tile as mma B fragments: column g of step x (rows 8 k + g) holds
 // the elements that the lane's K bytes stand for.
@@ -483,7 +457,7 @@ __device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& 
                            (row / p.G) * p.q_sn;
             constexpr int V = 16 / sizeof(T);
 #pragma unroll
-            for (int i = 0; i < G::kKCopies; ++i)
+            for (int i = 0; i < G::kKLoads; ++i)
 #pragma unroll
                 for (int y = 0; y < G::kKBytes; y += V) {
                     const uint4 w = *reinterpret_cast<const uint4*>(src + (i * 4 + c) * G::kKBytes + y);
@@ -536,13 +510,24 @@ struct Walk {
 };
 
 template <typename T, int CODE, int D, int R>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cache(CacheFwdParams p, float* ws) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
+    k_fwd_cache(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, CacheFwdParams p,
+                float* ws) {
     using G = Geo<D>;
     constexpr int kParts = parts<T>();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared<T, D, R>& sh = *reinterpret_cast<Shared<T, D, R>*>(smem_raw);
+    Shared<D, R>& sh = *reinterpret_cast<Shared<D, R>*>(
+        smem_raw + ((kRingAlign - (sm100::smem_u32(smem_raw) & (kRingAlign - 1))) & (kRingAlign - 1)));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
+    if (lane == 0) {
+        for (int x = 0; x < kStages; ++x) sm100::mbar_init(sm100::smem_u32(&sh.full[warp][x]), 1);
+        sm100::fence_mbar_init();
+        sm100::fence_proxy_async_smem();
+        sm100::prefetch_tensormap(&k_map);
+        sm100::prefetch_tensormap(&v_map);
+    }
+    __syncwarp();
 
     const Line line = line_total<D, R>(p, sh.sums);
     const int blocks = line_blocks(line.total, (int)gridDim.x);
@@ -555,104 +540,88 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
     const int rts = row_tiles<R>(p);
 
     uint8_t* const ring = &sh.ring[warp][0][0];
-    const uint32_t ring_at = sm100::smem_u32(ring), scales_at = sm100::smem_u32(&sh.scales[warp][0][0]);
+    const uint32_t ring_at = sm100::smem_u32(ring), full_at = sm100::smem_u32(&sh.full[warp][0]);
     const int page_mask = (1 << p.c.page_shift) - 1;
-    // this lane's bytes of a sub-block, from its first token
-    const uint32_t k_lane = (uint32_t)(g * p.c.k.s_t) + c * G::kKBytes, v_lane = (uint32_t)(2 * c * p.c.v.s_t) + g * G::kVBytes;
+    int k_at[G::kKLoads], v_at[2];  // this lane's bytes of a sub-block's first half
+#pragma unroll
+    for (int i = 0; i < G::kKLoads; ++i) k_at[i] = G::byte(G::token(g), (i * 4 + c) * G::kKBytes);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) v_at[r] = G::byte(G::token(2 * c + r), g * G::kVBytes);
+    int fill = 0, stage = 0;      // ring stages to refill and to use next
+    uint32_t phase = 0;           // of `stage`
+    bool dead = false;            // a wait ran out: no more copies, no more waits
 
     while (at < end) {
         const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
         const int hk = (int)((at - place) / t.groups);
         const int first = (int)((at - place) % t.groups);
         const int last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past
+
+        const int32_t* const table = p.c.table + t.b * p.c.table_stride;
+        // the table's entry for this lane's sub-block (lane % kSub) of a step, kUnread where none
+        // is needed; checked a step later, when it has arrived
+        auto page_of = [&](const Walk<D>& w) -> int {
+            const int j = w.j + 16 * (lane % G::kSub);
+            return w.x < last && j + 16 > w.lo(t) && j < w.hi(t) ? __ldg(table + (j >> p.c.page_shift)) : kUnread;
+        };
+        float pending = 0.f;  // this lane's scale of the step issued last, on its way
+        float* pending_at = nullptr;
+        auto issue = [&](const Walk<D>& w, int my_page) {
+            if (pending_at) *pending_at = pending;
+            pending_at = nullptr;
+            if (w.x >= last || dead) return;
+            if ((unsigned)my_page >= (unsigned)p.c.num_pages) {
+                if (my_page != kUnread) atomicOr(p.c.err, kErrBadPage);
+                my_page = -1;
+            }
+            const unsigned there = __ballot_sync(0xffffffffu, my_page >= 0) & ((1u << G::kSub) - 1);
+            if (lane < 2 * G::kSub) {  // lane: sub-block lane % kSub, of K or V
+                pending = kNoPage;
+                if (my_page >= 0)
+                    pending = __ldg((lane < G::kSub ? p.c.k.scale : p.c.v.scale) + (int64_t)my_page * p.c.Hk + hk);
+                pending_at = &sh.scales[warp][fill][lane];
+            }
+            const uint32_t bar = full_at + 8 * fill;
+            if (lane == 0) sm100::mbar_expect_tx(bar, 2 * G::kBox * __popc(there));
+            __syncwarp();
+            if (lane < G::kSub && my_page >= 0) {
+                const uint32_t dst = ring_at + fill * 2 * G::kSide + lane * G::kBox;
+                const int o = (w.j + 16 * lane) & page_mask;
+                sm100::tma_load_4d(dst, &k_map, bar, 0, o, hk, my_page);
+                sm100::tma_load_4d(dst + G::kSide, &v_map, bar, 0, o, hk, my_page);
+            }
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+        };
+
+        Walk<D> ahead(t, first, warp), now(t, first, warp);
+        int page = page_of(ahead);
         Query<T, D, R> q;
         load_query<T, D, R>(p, t, hk, q);
         State<D, R> st;
         st.clear();
-
-        // the page of this lane's sub-block (lane % kSub) of a step, -1 where none is needed
-        auto page_of = [&](const Walk<D>& w) -> int {
-            const int j = w.j + 16 * (lane % G::kSub);
-            return w.x < last && j + 16 > w.lo(t) && j < w.hi(t) ? cache_page(p.c, t.b, j) : -1;
-        };
-        auto issue = [&](const Walk<D>& w, int my_page, int stage) {
-            if (w.x < last) {
-                const int lo = w.lo(t), hi = w.hi(t);
-                const uint32_t kd = ring_at + stage * 2 * G::kSide + lane * G::kKBytes;
-                const uint32_t vd = ring_at + stage * 2 * G::kSide + G::kSide + lane * G::kVBytes;
-                const bool whole = w.j >= lo && w.j + 16 * G::kSub <= hi && __all_sync(0xffffffffu, my_page >= 0);
-#pragma unroll
-                for (int sb = 0; sb < G::kSub; ++sb) {
-                    const int pid = __shfl_sync(0xffffffffu, my_page, sb);
-                    const int j = w.j + 16 * sb, place = j & page_mask;
-                    const uint8_t *kp = p.c.k.codes, *vp = p.c.v.codes;
-                    if (pid >= 0) {
-                        kp += pid * p.c.k.s_p + hk * p.c.k.s_h + place * p.c.k.s_t + k_lane;
-                        vp += pid * p.c.v.s_p + hk * p.c.v.s_h + place * p.c.v.s_t + v_lane;
-                    }
-                    const uint32_t k8 = (uint32_t)(8 * p.c.k.s_t), v1 = (uint32_t)p.c.v.s_t, v8 = 8 * v1;
-                    if (whole) {
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                            for (int i = 0; i < G::kKCopies; ++i)
-                                copy_async<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes,
-                                                       kp + nt * k8 + i * 4 * G::kKBytes);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            copy_async<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes, vp + (r & 1) * v1 + (r >> 1) * v8);
-                    } else {
-#pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            const int o = j + 8 * nt + g;
-                            const bool there = pid >= 0 && o >= lo && o < hi;
-#pragma unroll
-                            for (int i = 0; i < G::kKCopies; ++i)
-                                copy_async_or_zero<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes,
-                                                               kp + (there ? nt * k8 + i * 4 * G::kKBytes : 0), there);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int o = j + 2 * c + (r & 1) + 8 * (r >> 1);
-                            const bool there = pid >= 0 && o >= lo && o < hi;
-                            copy_async_or_zero<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes,
-                                                       vp + (there ? (r & 1) * v1 + (r >> 1) * v8 : 0), there);
-                        }
-                    }
-                }
-                if (lane < 2 * G::kSub) {  // lane: sub-block lane % kSub, of K or V
-                    const uint32_t dst = scales_at + (stage * 2 * G::kSub + lane) * 4;
-                    if (my_page >= 0)
-                        copy_async<4>(dst, (lane < G::kSub ? p.c.k.scale : p.c.v.scale) + (int64_t)my_page * p.c.Hk + hk);
-                    else
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(kNoPage) : "memory");
-                }
-            }
-            copy_commit();
-        };
-
-        Walk<D> ahead(t, first, warp), now(t, first, warp);
-        int page = page_of(ahead), fill = 0, stage = 0;
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            issue(ahead, page, fill++);
+            issue(ahead, page);
             ahead.next(t);
             page = page_of(ahead);
         }
         for (; now.x < last; now.next(t)) {
-            copy_wait<kStages - 2>();
-            __syncwarp();  // the other lanes' scales are there, and every lane is done with the stage refilled next
-            issue(ahead, page, fill);
-            fill = fill + 1 == kStages ? 0 : fill + 1;
+            if (!dead && !sm100::mbar_wait_bounded(full_at + 8 * stage, phase, kCacheWaitCycles)) {
+                dead = true;
+                if (lane == 0) atomicOr(p.c.err, kErrTimeout);
+            }
+            dead = __any_sync(0xffffffffu, dead);  // and every lane is done with the stage refilled next
+            issue(ahead, page);
             ahead.next(t);
             page = page_of(ahead);
             const int lo = now.lo(t), hi = now.hi(t);
-            const uint8_t* kd = ring + stage * 2 * G::kSide + lane * G::kKBytes;
-            const uint8_t* vd = ring + stage * 2 * G::kSide + G::kSide + lane * G::kVBytes;
+            const uint8_t* kd = ring + stage * 2 * G::kSide;
+            const uint8_t* vd = kd + G::kSide;
             const float* sc = &sh.scales[warp][stage][0];
             stage = stage + 1 == kStages ? 0 : stage + 1;
+            phase ^= stage == 0;
             if (now.j + 16 * G::kSub <= lo || now.j >= hi) continue;
-            // S^T = K Q^T: e[k][sb][2 x + y]: row 8 k + 2 c + y, token 16 sb + 8 x + g
+            // S^T = K Q^T: e[k][sb][2 x + y]: row 8 k + 2 c + y, token 16 sb + 8 x + token(g)
             float e[R][G::kSub][4];
             auto scores = [&]() {
 #pragma unroll
@@ -660,11 +629,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
 #pragma unroll
                     for (int k = 0; k < R; ++k) e[k][sb][0] = e[k][sb][1] = e[k][sb][2] = e[k][sb][3] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < G::kKCopies; ++i) {
+                    for (int i = 0; i < G::kKLoads; ++i) {
                         uint32_t w[2][G::kKBytes / 4];
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt)
-                            load_words<G::kKBytes>(kd + ((sb * 2 + nt) * G::kKCopies + i) * 32 * G::kKBytes, w[nt]);
+                            load_words<G::kKBytes>(kd + sb * G::kBox + 8 * nt * D + k_at[i], w[nt]);
 #pragma unroll
                         for (int y = 0; y < G::kKBytes / 4; ++y) {
                             uint32_t a[4];
@@ -719,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
                             for (int sb = 0; sb < G::kSub; ++sb)
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
-                                    const int tok = now.j + 16 * sb + 8 * x + g;
+                                    const int tok = now.j + 16 * sb + 8 * x + G::token(g);
                                     const bool sees = tok <= pos && tok >= lo && tok < hi && ks[sb] != kNoPage &&
                                                       (p.window < 0 || tok >= pos - p.window || tok < p.n_global);
                                     if (!sees) e[k][sb][2 * x + y] = -INFINITY;
@@ -784,7 +753,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
                     }
                 uint32_t v[4][(G::kVBytes + 3) / 4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) load_words<G::kVBytes>(vd + (sb * 4 + r) * 32 * G::kVBytes, v[r]);
+                for (int r = 0; r < 4; ++r) {
+                    load_words<G::kVBytes>(vd + sb * G::kBox + 8 * (r >> 1) * D + v_at[r & 1], v[r]);
+                    if (!full) {  // tokens that no row may see: their codes may be anything
+                        const int tok = now.j + 16 * sb + 8 * (r >> 1) + G::token(2 * c + (r & 1));
+                        if (tok < lo || tok >= hi || ks[sb] == kNoPage) {
+#pragma unroll
+                            for (int y = 0; y < (G::kVBytes + 3) / 4; ++y) v[r][y] = 0;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int y = 0; y < G::kVBytes / 4; ++y)
 #pragma unroll
@@ -800,8 +778,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
                     }
             }
         }
-        copy_wait<0>();
-        __syncwarp();
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -824,11 +800,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>()) k_fwd_cach
 }
 
 // Block x: segment x (entry x / Hk). The pieces of a segment that several blocks
-// worked on are added up, each warp taking every fourth.
+// worked on are added up: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
-    __shared__ JoinO<D, R> join;
-    __shared__ JoinMl<R> ml;
+    __shared__ float tops[8 * R], sums_l[8 * R];
     __shared__ int64_t sums[kThreads + 1];
     const int warp = threadIdx.x >> 5;
     const Line line = line_total<D, R>(p, sums);
@@ -849,21 +824,101 @@ __global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, c
     const int x0 = block_of(s0), x1 = block_of(s1);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // every block, so that this kernel ends after the first
     if (x0 == x1) return;
-    State<D, R> st;
-    st.clear();
-    for (int x = x0 + warp; x <= x1; x += kWarps)
-        add_piece<D, R>(ws + ((int64_t)x * 2 + (x == x0)) * piece_floats<D, R>(), st, t.rows);
-    join_warps<D, R>(st, ml, join);
-    if (warp == 0) write_rows<T, D, R>(p, t, hk, st);
+    // the rows' references and sums: a warp every fourth row, its lanes over the pieces
+    const int np = x1 - x0 + 1, lane = threadIdx.x & 31;
+    auto piece = [&](int i) { return ws + ((int64_t)(x0 + i) * 2 + (i == 0)) * piece_floats<D, R>(); };
+    for (int row = warp; row < t.rows; row += kWarps) {
+        float top = kNone, l = 0.f;
+        for (int i = lane; i < np; i += 32) top = fmaxf(top, piece(i)[row]);
+#pragma unroll
+        for (int z = 1; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+        for (int i = lane; i < np; i += 32) l += ex2(piece(i)[row] - top) * piece(i)[8 * R + row];
+#pragma unroll
+        for (int z = 1; z < 32; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+        if (lane == 0) {
+            tops[row] = top;
+            sums_l[row] = l;
+        }
+    }
+    __syncthreads();
+    // a thread: 2 rows x 2 elements at a time
+    constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32;
+#pragma unroll 1
+    for (int u = threadIdx.x; u < kUnits; u += kThreads) {
+        const int k = u / (N * 32), i = u / 32 % N, g = (u & 31) >> 2, row = 8 * k + 2 * (u & 3);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < t.rows) {
+            const float top0 = tops[row], top1 = row + 1 < t.rows ? tops[row + 1] : 0.f;
+#pragma unroll 4
+            for (int x = 0; x < np; ++x) {
+                const float* src = piece(x);
+                const float2 m = *reinterpret_cast<const float2*>(src + row);
+                const float4 v = reinterpret_cast<const float4*>(src + 16 * R)[u];
+                const float w0 = ex2(m.x - top0), w1 = row + 1 < t.rows ? ex2(m.y - top1) : 0.f;
+                o.x += v.x * w0;
+                o.y += v.y * w1;
+                o.z += v.z * w0;
+                o.w += v.w * w1;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int in_tile = row + e, r = t.first_row + in_tile;
+            if (r >= p.m * p.G) continue;
+            const int q = r / p.G, h = hk * p.G + r % p.G;
+            const bool there = in_tile < t.rows && sums_l[in_tile] != 0.f;
+            const float inv = there ? 1.f / sums_l[in_tile] : 0.f;
+            const float a = there ? (e ? o.y : o.x) * inv : 0.f, b = there ? (e ? o.w : o.z) * inv : 0.f;
+            T* out = static_cast<T*>(p.out) + t.b * p.o_sb + h * p.o_sh + q * p.o_sn + Geo<D>::kVBytes * g + 2 * i;
+            if constexpr (std::is_same<T, float>::value)
+                *reinterpret_cast<float2*>(out) = make_float2(a, b);
+            else
+                *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(a, b);
+            if (p.lse && g == 0 && i == 0)
+                p.lse[((int64_t)t.b * p.H + h) * p.m + q] = there ? (tops[in_tile] + log2f(sums_l[in_tile])) * kLn2 : -INFINITY;
+        }
+    }
+}
+
+// {d, token, head, page} bytes, box {d, 16, 1, 1}.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+cudaError_t side_map(CUtensorMap* map, const CacheSide& side, const CacheView& c, int d) {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, []() {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    if (!fn) return cudaErrorNotSupported;
+    const uint64_t page = 1u << c.page_shift, st = side.s_t;
+    const uint64_t sh = c.Hk > 1 ? side.s_h : st * page, sp = c.num_pages > 1 ? side.s_p : sh * c.Hk;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, page, (cuuint64_t)c.Hk, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {st, sh, sp};
+    const cuuint32_t box[4] = {(cuuint32_t)d, 16, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, side.codes, dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <typename T, int CODE, int D, int R>
 cudaError_t fwd_r(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t s) {
-    const int smem = (int)sizeof(Shared<T, D, R>);
-    cudaError_t e = cudaFuncSetAttribute(k_fwd_cache<T, CODE, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = (int)sizeof(Shared<D, R>) + kRingAlign - 16;
+    CUtensorMap k_map, v_map;
+    cudaError_t e = side_map(&k_map, p.c.k, p.c, D);
+    if (e == cudaSuccess) e = side_map(&v_map, p.c.v, p.c, D);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(k_fwd_cache<T, CODE, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = num_sms * blocks_per_sm<T, D, R>();
-    k_fwd_cache<T, CODE, D, R><<<grid, kThreads, smem, counted(s)>>>(p, ws);
+    k_fwd_cache<T, CODE, D, R><<<grid, kThreads, smem, counted(s)>>>(k_map, v_map, p, ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)p.B * row_tiles<R>(p) * p.c.Hk));

@@ -1399,8 +1399,8 @@ int check_cache_side(const spattn_tensor* t, const char* name, const int64_t* sh
     if (((uintptr_t)t->data) % 16 != 0)
         return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s.data is not 16-byte aligned", name);
     for (int x = 0; x < 3; ++x)
-        if (t->shape[x] > 1 && (t->stride[x] % 16 != 0 || t->stride[x] < 0))
-            return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s stride[%d] is negative or not a multiple of 16 bytes", name, x);
+        if (t->shape[x] > 1 && (t->stride[x] % 16 != 0 || t->stride[x] < 16 || t->stride[x] >= (int64_t)1 << 39))
+            return fail(SPATTN_ERR_UNSUPPORTED, "cache.%s stride[%d] is not a positive multiple of 16 bytes below 2^39", name, x);
     auto bs = [&](int x) { return t->shape[x] == 1 ? 0 : t->stride[x]; };
     out->codes = static_cast<uint8_t*>(t->data);
     out->scale = const_cast<float*>(scale);
