@@ -593,34 +593,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             fill = fill + 1 == kStages ? 0 : fill + 1;
         };
 
-        Walk<D> ahead(t, first, warp), now(t, first, warp);
-        int page = page_of(ahead);
         Query<T, D, R> q;
-        load_query<T, D, R>(p, t, hk, q);
         State<D, R> st;
-        st.clear();
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            issue(ahead, page);
-            ahead.next(t);
-            page = page_of(ahead);
-        }
-        for (; now.x < last; now.next(t)) {
-            if (!dead && !sm100::mbar_wait_bounded(full_at + 8 * stage, phase, kCacheWaitCycles)) {
-                dead = true;
-                if (lane == 0) atomicOr(p.c.err, kErrTimeout);
-            }
-            dead = __any_sync(0xffffffffu, dead);  // and every lane is done with the stage refilled next
-            issue(ahead, page);
-            ahead.next(t);
-            page = page_of(ahead);
-            const int lo = now.lo(t), hi = now.hi(t);
-            const uint8_t* kd = ring + stage * 2 * G::kSide;
-            const uint8_t* vd = kd + G::kSide;
-            const float* sc = &sh.scales[warp][stage][0];
-            stage = stage + 1 == kStages ? 0 : stage + 1;
-            phase ^= stage == 0;
-            if (now.j + 16 * G::kSub <= lo || now.j >= hi) continue;
+        auto step = [&](const uint8_t* kd, const uint8_t* vd, const float* sc, int lo, int hi, int j0, auto all) {
+            constexpr bool full = decltype(all)::value;  // every row attends to every token of the step
             // S^T = K Q^T: e[k][sb][2 x + y]: row 8 k + 2 c + y, token 16 sb + 8 x + token(g)
             float e[R][G::kSub][4];
             auto scores = [&]() {
@@ -652,20 +628,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             };
             scores();
             // to exponents x + log2 vs - m, -inf where a row does not attend
-            bool odd = false;  // a sub-block without a page or with a V scale of 0
             float ks[G::kSub], lv[G::kSub], inv_vs[G::kSub];
 #pragma unroll
             for (int sb = 0; sb < G::kSub; ++sb) {
                 const float vs = sc[G::kSub + sb];
+                const bool none = !full && vs < kMinScale;
                 ks[sb] = sc[sb];
-                odd |= vs < kMinScale;
-                lv[sb] = vs < kMinScale ? 0.f : sm100::lg2(vs);
-                inv_vs[sb] = vs < kMinScale ? 1.f : __frcp_rn(vs);
+                lv[sb] = none ? 0.f : sm100::lg2(vs);
+                inv_vs[sb] = none ? 1.f : __frcp_rn(vs);
             }
-            const bool in_a = now.x < t.na;
-            const int j_end = now.j + 16 * G::kSub;
-            const bool full = !odd && (in_a ? j_end <= t.full_a
-                                            : j_end <= t.full_hi && (now.j >= t.full_lo || j_end <= t.full_a));
             auto exponents = [&](bool from_zero) {
 #pragma unroll
                 for (int k = 0; k < R; ++k)
@@ -688,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                             for (int sb = 0; sb < G::kSub; ++sb)
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
-                                    const int tok = now.j + 16 * sb + 8 * x + G::token(g);
+                                    const int tok = j0 + 16 * sb + 8 * x + G::token(g);
                                     const bool sees = tok <= pos && tok >= lo && tok < hi && ks[sb] != kNoPage &&
                                                       (p.window < 0 || tok >= pos - p.window || tok < p.n_global);
                                     if (!sees) e[k][sb][2 * x + y] = -INFINITY;
@@ -740,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             // O^T += V^T P^T
 #pragma unroll
             for (int sb = 0; sb < G::kSub; ++sb) {
-                if (odd && sc[G::kSub + sb] < kMinScale) continue;
+                if (!full && sc[G::kSub + sb] < kMinScale) continue;
                 uint32_t pb[kParts][R][2];
 #pragma unroll
                 for (int k = 0; k < R; ++k)
@@ -756,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 for (int r = 0; r < 4; ++r) {
                     load_words<G::kVBytes>(vd + sb * G::kBox + 8 * (r >> 1) * D + v_at[r & 1], v[r]);
                     if (!full) {  // tokens that no row may see: their codes may be anything
-                        const int tok = now.j + 16 * sb + 8 * (r >> 1) + G::token(2 * c + (r & 1));
+                        const int tok = j0 + 16 * sb + 8 * (r >> 1) + G::token(2 * c + (r & 1));
                         if (tok < lo || tok >= hi || ks[sb] == kNoPage) {
 #pragma unroll
                             for (int y = 0; y < (G::kVBytes + 3) / 4; ++y) v[r][y] = 0;
@@ -777,6 +748,44 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                             for (int w = 0; w < kParts; ++w) mma_f16(st.o[k][2 * y + z], a, pb[w][k][0], pb[w][k][1]);
                     }
             }
+        };
+        Walk<D> ahead(t, first, warp), now(t, first, warp);
+        int page = page_of(ahead);
+        load_query<T, D, R>(p, t, hk, q);
+        st.clear();
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            issue(ahead, page);
+            ahead.next(t);
+            page = page_of(ahead);
+        }
+        for (; now.x < last; now.next(t)) {
+            if (!dead && !sm100::mbar_wait_bounded(full_at + 8 * stage, phase, kCacheWaitCycles)) {
+                dead = true;
+                if (lane == 0) atomicOr(p.c.err, kErrTimeout);
+            }
+            dead = __any_sync(0xffffffffu, dead);  // and every lane is done with the stage refilled next
+            issue(ahead, page);
+            ahead.next(t);
+            page = page_of(ahead);
+            const int lo = now.lo(t), hi = now.hi(t);
+            const uint8_t* kd = ring + stage * 2 * G::kSide;
+            const uint8_t* vd = kd + G::kSide;
+            const float* sc = &sh.scales[warp][stage][0];
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            phase ^= stage == 0;
+            if (now.j + 16 * G::kSub <= lo || now.j >= hi) continue;
+            bool odd = false;  // a sub-block without a page or with a V scale of 0
+#pragma unroll
+            for (int sb = 0; sb < G::kSub; ++sb) odd |= sc[G::kSub + sb] < kMinScale;
+            const int j_end = now.j + 16 * G::kSub;
+            const bool full = !odd && (now.x < t.na ? j_end <= t.full_a
+                                                    : j_end <= t.full_hi && (now.j >= t.full_lo || j_end <= t.full_a));
+            // two copies of the step, so that the common one carries no masks
+            if (full)
+                step(kd, vd, sc, lo, hi, now.j, std::true_type{});
+            else
+                step(kd, vd, sc, lo, hi, now.j, std::false_type{});
         }
 #pragma unroll
         for (int k = 0; k < R; ++k)
