@@ -24,14 +24,14 @@
 // largest exponent - 5), so that most steps need no exchange between lanes.
 //
 // Streaming. The kernel is bound by HBM at long caches: each code is read once.
-// Each warp has a ring of its own in shared memory, filled by TMA: a copy brings
-// 16 tokens of one page (4-D map {d, token, head, page}, any strides), swizzled so
-// that the fragment loads meet few bank conflicts. A step is kSub such sub-blocks
-// of K and of V. Fragments need no exchange between lanes: any order of the head
-// dim and of the tokens does for a product as long as both sides use the same, so
-// K fragments are 4 neighbouring codes of a token, and V fragments byte columns of
-// four tokens. The page table's entry and the page's scales are read a step
-// before they are used.
+// A producer warp fills a ring in shared memory by TMA: a copy brings 16 tokens
+// of one page (4-D map {d, token, head, page}, any strides), swizzled so that the
+// fragment loads meet few bank conflicts; a stage is kSub such sub-blocks of K and
+// of V for each of the other warps. It reads the page table two stages ahead and
+// the pages' scales one, and runs on over the ends of segments. Fragments need no
+// exchange between lanes: any order of the head dim and of the tokens does for a
+// product as long as both sides use the same, so K fragments are 4 neighbouring
+// codes of a token, and V fragments byte columns of four tokens.
 //
 // Work. All segments' steps form one line, which the grid's blocks share evenly
 // (they know it from the lengths alone), so that one long sequence among short
@@ -49,7 +49,9 @@ namespace {
 
 using sm100::ex2;
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 7;                         // that compute
+constexpr int kThreads = (kWarps + 1) * 32;       // and the producer
+constexpr int kJoinThreads = 128;
 constexpr float kNone = -1e30f;      // reference of a row without a token so far
 constexpr float kRescaleAt = 12.f;   // largest exponent of a weight before the reference moves
 constexpr float kHeadroom = 5.f;     // exponent of the largest weight after it moved
@@ -139,9 +141,9 @@ __host__ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p) {
 struct Line {
     int64_t total;
 };
-template <int D, int R>
-__device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[kThreads + 1]) {
-    const int entries = p.B * row_tiles<R>(p), per = (entries + kThreads - 1) / (kThreads);
+template <int D, int R, int NT>
+__device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[NT + 1]) {
+    const int entries = p.B * row_tiles<R>(p), per = (entries + NT - 1) / (NT);
     const int tid = threadIdx.x;
     int64_t mine = 0;
     for (int e = tid * per; e < entries && e < (tid + 1) * per; ++e)
@@ -161,14 +163,14 @@ __device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[kThreads + 1
     __syncthreads();
     sums[tid + 1] = x + before;
     __syncthreads();
-    return Line{sums[kThreads] * p.c.Hk};
+    return Line{sums[NT] * p.c.Hk};
 }
 // The entry that holds place `at` < total, and its first place.
-template <int D, int R>
-__device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[kThreads + 1], int64_t at, int* entry,
+template <int D, int R, int NT>
+__device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[NT + 1], int64_t at, int* entry,
                           int64_t* first) {
-    const int per = (p.B * row_tiles<R>(p) + kThreads - 1) / (kThreads);
-    int lo = 0, hi = kThreads - 1;  // the thread whose entries hold it
+    const int per = (p.B * row_tiles<R>(p) + NT - 1) / (NT);
+    int lo = 0, hi = NT - 1;  // the thread whose entries hold it
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (sums[mid + 1] * p.c.Hk > at) hi = mid;
@@ -283,27 +285,27 @@ struct State {
     }
 };
 
-// Where the warps' states meet. o may lie over the ring: join_warps writes it
-// after a barrier, and makes the writes known to the copies that refill it.
+// Where the computing warps' states meet.
 template <int D, int R>
 struct JoinO {
-    float4 o[2][R * Geo<D>::kSteps][32];
+    float4 o[3][R * Geo<D>::kSteps][32];
 };
 template <int R>
 using JoinMl = float[kWarps][2][8 * R];
 
-// The block's warps' states (l summed over the row's lanes) joined into warp 0's.
+// The computing warps' states (l summed over the row's lanes) joined into warp 0's.
 template <int D, int R>
 __device__ __forceinline__ void join_warps(State<D, R>& s, JoinMl<R>& ml, JoinO<D, R>& sh) {
     constexpr int N = Geo<D>::kSteps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
+    auto sync = []() { sm100::named_sync(1, kWarps * 32); };
     if (lane < 4) {
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) ml[warp][0][8 * k + 2 * c + e] = s.m[k][e];
     }
-    __syncthreads();
+    sync();
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         float top[2];
@@ -322,23 +324,26 @@ __device__ __forceinline__ void join_warps(State<D, R>& s, JoinMl<R>& ml, JoinO<
             ml[warp][1][8 * k + 2 * c + 1] = s.l[k][1];
         }
     }
-    if (warp >= 2) {
+    // 7 -> 4 -> 2 -> 1: after the first round a warp writes the buffer that only it has read
+    auto give = [&](int buf) {
 #pragma unroll
-        for (int x = 0; x < R * N; ++x) sh.o[warp - 2][x][lane] = s.get(x / N, x % N);
-    }
-    __syncthreads();
-    if (warp < 2) {
+        for (int x = 0; x < R * N; ++x) sh.o[buf][x][lane] = s.get(x / N, x % N);
+    };
+    auto take = [&](int buf) {
 #pragma unroll
-        for (int x = 0; x < R * N; ++x) s.add(x / N, x % N, sh.o[warp][x][lane], 1.f, 1.f);
-        if (warp == 1) {  // each lane writes what only it has read
-#pragma unroll
-            for (int x = 0; x < R * N; ++x) sh.o[1][x][lane] = s.get(x / N, x % N);
-        }
-    }
-    __syncthreads();
+        for (int x = 0; x < R * N; ++x) s.add(x / N, x % N, sh.o[buf][x][lane], 1.f, 1.f);
+    };
+    static_assert(kWarps == 7, "the rounds below");
+    if (warp >= 4) give(warp - 4);
+    sync();
+    if (warp >= 1 && warp <= 3) take(warp - 1);
+    if (warp == 2 || warp == 3) give(warp - 1);
+    sync();
+    if (warp <= 1) take(warp + 1);
+    if (warp == 1) give(0);
+    sync();
+    if (warp == 0) take(0);
     if (warp == 0) {
-#pragma unroll
-        for (int x = 0; x < R * N; ++x) s.add(x / N, x % N, sh.o[1][x][lane], 1.f, 1.f);
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -348,8 +353,7 @@ __device__ __forceinline__ void join_warps(State<D, R>& s, JoinMl<R>& ml, JoinO<
                 for (int w = 0; w < kWarps; ++w) s.l[k][e] += ml[w][1][8 * k + 2 * c + e];
             }
     }
-    sm100::fence_proxy_async_smem();
-    __syncthreads();  // the buffers may be written again
+    sync();  // the buffers may be written again
 }
 
 // Warp 0: the finished rows of a tile. Those behind the sequence's queries get
@@ -415,23 +419,24 @@ template <typename T>
 constexpr int parts() {
     return std::is_same<T, float>::value ? 2 : 1;
 }
-constexpr int kStages = 3;  // of the ring
-// Blocks an SM holds (50 KB of shared memory each) with 128, 168 or 255 registers
-// a thread; O, Q and the scores take `held` of them.
+// Blocks an SM holds: with 128 registers a thread two, else one. O, Q and the
+// scores take `held` of them.
 template <typename T, int D, int R>
 constexpr int blocks_per_sm() {
     const int held = (D / 4 + parts<T>() * D / 8 + 4 * Geo<D>::kSub) * R;
-    return R == 1 ? 4 : held <= 104 ? 3 : 2;
+    return held <= 68 ? 2 : 1;
+}
+template <typename T, int D, int R>
+constexpr int stages() {  // of the ring, 28 KB each
+    return blocks_per_sm<T, D, R>() == 2 ? 3 : 5;
 }
 
-template <int D, int R>
+template <int D, int R, int S>
 struct Shared {
-    union {
-        uint8_t ring[kWarps][kStages][2 * Geo<D>::kSide];  // a stage: K, then V
-        JoinO<D, R> join;
-    };
-    float scales[kWarps][kStages][2 * Geo<D>::kSub];  // K, V of each sub-block
-    uint64_t full[kWarps][kStages];
+    uint8_t ring[S][kWarps][2 * Geo<D>::kSide];  // a warp's part of a stage: K, then V
+    JoinO<D, R> join;
+    float scales[S][2][kWarps * Geo<D>::kSub];  // K, V of each sub-block
+    uint64_t full[S], empty[S];
     JoinMl<R> ml;
     int64_t sums[kThreads + 1];
 };
@@ -494,12 +499,13 @@ __device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& 
     }
 }
 
-// A warp's walk over the groups of a tile: group x, its first token j.
+// A walk over the groups of a tile: group x, its first token j.
 template <int D>
 struct Walk {
     int x, j;
-    __device__ __forceinline__ Walk(const Tile& t, int x0, int warp) : x(x0) {
-        j = (x0 < t.na ? x0 : t.b_first + x0 - t.na) * Geo<D>::kGroup + warp * Geo<D>::kSub * 16;
+    __device__ __forceinline__ void begin(const Tile& t, int x0) {
+        x = x0;
+        j = (x0 < t.na ? x0 : t.b_first + x0 - t.na) * Geo<D>::kGroup;
     }
     __device__ __forceinline__ void next(const Tile& t) {
         ++x;
@@ -509,93 +515,162 @@ struct Walk {
     __device__ __forceinline__ int hi(const Tile& t) const { return x < t.na ? t.a_hi : t.b_hi; }
 };
 
+// A block's part of the line, segment by segment.
+template <int D, int R>
+struct Part {
+    int64_t at, end, place;  // next step, one past the last, the entry's first
+    int entry;
+    Tile t;
+    int hk, first, last;  // of the current segment
+    __device__ __forceinline__ bool open(const CacheFwdParams& p, int rts) {  // the segment that holds `at`
+        if (at >= end) return false;
+        t = make_tile<D, R>(p, entry / rts, entry % rts);
+        hk = (int)((at - place) / t.groups);
+        first = (int)((at - place) % t.groups);
+        last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past
+        return true;
+    }
+    __device__ __forceinline__ void close(const CacheFwdParams& p) {  // on to the next one
+        at += last - first;
+        if (at >= place + (int64_t)t.groups * p.c.Hk) {
+            place += (int64_t)t.groups * p.c.Hk;
+            ++entry;
+        }
+    }
+};
+
+// The producer warp: lane x brings sub-block x of each stage.
+template <int D, int R, int S>
+__device__ __forceinline__ void produce(const CUtensorMap& k_map, const CUtensorMap& v_map, const CacheFwdParams& p,
+                                        Shared<D, R, S>& sh, Part<D, R> part, int rts) {
+    using G = Geo<D>;
+    constexpr int kN = kWarps * G::kSub;  // sub-blocks of a stage
+    const int lane = threadIdx.x & 31;
+    const int page_mask = (1 << p.c.page_shift) - 1;
+    const uint32_t ring_at = sm100::smem_u32(&sh.ring[0][0][0]), full_at = sm100::smem_u32(&sh.full[0]),
+                   empty_at = sm100::smem_u32(&sh.empty[0]);
+    // a step on its way: the table's entry (kUnread: none needed), then the page's scales
+    struct Step {
+        int raw, j, hk;
+        bool more;
+    };
+    bool open = part.open(p, rts);
+    Walk<D> w;
+    if (open) w.begin(part.t, part.first);
+    auto look_up = [&]() -> Step {
+        Step s{kUnread, 0, 0, open};
+        if (!open) return s;
+        s.j = w.j + 16 * lane;
+        s.hk = part.hk;
+        if (lane < kN && s.j + 16 > w.lo(part.t) && s.j < w.hi(part.t))
+            s.raw = __ldg(p.c.table + part.t.b * p.c.table_stride + (s.j >> p.c.page_shift));
+        w.next(part.t);
+        if (w.x >= part.last) {
+            part.close(p);
+            open = part.open(p, rts);
+            if (open) w.begin(part.t, part.first);
+        }
+        return s;
+    };
+    auto scales_of = [&](Step& s, float& ks, float& vs) {
+        ks = vs = kNoPage;
+        if ((unsigned)s.raw >= (unsigned)p.c.num_pages) {
+            if (s.raw != kUnread) atomicOr(p.c.err, kErrBadPage);
+            s.raw = -1;
+        } else {
+            const int64_t at = (int64_t)s.raw * p.c.Hk + s.hk;
+            ks = __ldg(p.c.k.scale + at);
+            vs = __ldg(p.c.v.scale + at);
+        }
+    };
+    Step now = look_up(), next = look_up();
+    float ks, vs, ks_next = 0.f, vs_next = 0.f;
+    scales_of(now, ks, vs);
+    int stage = 0;
+    uint32_t phase = 1;  // the first round's waits pass at once
+    bool dead = false;
+    while (now.more) {
+        if (!dead && !sm100::mbar_wait_bounded(empty_at + 8 * stage, phase, kCacheWaitCycles)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        const unsigned there = __ballot_sync(0xffffffffu, now.raw >= 0);
+        const uint32_t bar = full_at + 8 * stage;
+        if (now.raw >= 0) {
+            const uint32_t dst = ring_at + ((stage * kWarps + lane / G::kSub) * 2 * G::kSub + lane % G::kSub) * G::kBox;
+            sm100::tma_load_4d(dst, &k_map, bar, 0, now.j & page_mask, now.hk, now.raw);
+            sm100::tma_load_4d(dst + G::kSide, &v_map, bar, 0, now.j & page_mask, now.hk, now.raw);
+        }
+        if (next.more) scales_of(next, ks_next, vs_next);
+        const Step after = look_up();
+        if (lane < kN) {
+            sh.scales[stage][0][lane] = ks;
+            sh.scales[stage][1][lane] = vs;
+        }
+        __syncwarp();
+        // the copies above may have finished already: the barrier's phase waits for this arrival
+        if (lane == 0) sm100::mbar_expect_tx(bar, 2 * G::kBox * __popc(there));
+        stage = stage + 1 == S ? 0 : stage + 1;
+        phase ^= stage == 0;
+        now = next;
+        next = after;
+        ks = ks_next;
+        vs = vs_next;
+    }
+    if (dead && lane == 0) atomicOr(p.c.err, kErrTimeout);
+}
+
 template <typename T, int CODE, int D, int R>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
     k_fwd_cache(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, CacheFwdParams p,
                 float* ws) {
     using G = Geo<D>;
-    constexpr int kParts = parts<T>();
+    constexpr int kParts = parts<T>(), kStages = stages<T, D, R>();
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shared<D, R>& sh = *reinterpret_cast<Shared<D, R>*>(
+    using Sh = Shared<D, R, kStages>;
+    Sh& sh = *reinterpret_cast<Sh*>(
         smem_raw + ((kRingAlign - (sm100::smem_u32(smem_raw) & (kRingAlign - 1))) & (kRingAlign - 1)));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
-    if (lane == 0) {
-        for (int x = 0; x < kStages; ++x) sm100::mbar_init(sm100::smem_u32(&sh.full[warp][x]), 1);
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < kStages; ++x) {
+            sm100::mbar_init(sm100::smem_u32(&sh.full[x]), 1);
+            sm100::mbar_init(sm100::smem_u32(&sh.empty[x]), kWarps);
+        }
         sm100::fence_mbar_init();
         sm100::fence_proxy_async_smem();
         sm100::prefetch_tensormap(&k_map);
         sm100::prefetch_tensormap(&v_map);
     }
-    __syncwarp();
 
-    const Line line = line_total<D, R>(p, sh.sums);
+    const Line line = line_total<D, R, kThreads>(p, sh.sums);  // (with barriers)
     const int blocks = line_blocks(line.total, (int)gridDim.x);
     if ((int)blockIdx.x >= blocks) return;
-    int64_t at = line_start(line.total, blocks, blockIdx.x);
-    const int64_t end = line_start(line.total, blocks, blockIdx.x + 1);
-    int entry;
-    int64_t place;
-    line_find<D, R>(p, sh.sums, at, &entry, &place);
     const int rts = row_tiles<R>(p);
+    Part<D, R> part;
+    part.at = line_start(line.total, blocks, blockIdx.x);
+    part.end = line_start(line.total, blocks, blockIdx.x + 1);
+    line_find<D, R, kThreads>(p, sh.sums, part.at, &part.entry, &part.place);
+    if (warp == kWarps) {
+        produce<D, R, kStages>(k_map, v_map, p, sh, part, rts);
+        return;
+    }
 
-    uint8_t* const ring = &sh.ring[warp][0][0];
-    const uint32_t ring_at = sm100::smem_u32(ring), full_at = sm100::smem_u32(&sh.full[warp][0]);
-    const int page_mask = (1 << p.c.page_shift) - 1;
+    const uint8_t* const ring = &sh.ring[0][warp][0];
+    const uint32_t full_at = sm100::smem_u32(&sh.full[0]), empty_at = sm100::smem_u32(&sh.empty[0]);
     int k_at[G::kKLoads], v_at[2];  // this lane's bytes of a sub-block's first half
 #pragma unroll
     for (int i = 0; i < G::kKLoads; ++i) k_at[i] = G::byte(G::token(g), (i * 4 + c) * G::kKBytes);
 #pragma unroll
     for (int r = 0; r < 2; ++r) v_at[r] = G::byte(G::token(2 * c + r), g * G::kVBytes);
-    int fill = 0, stage = 0;      // ring stages to refill and to use next
-    uint32_t phase = 0;           // of `stage`
-    bool dead = false;            // a wait ran out: no more copies, no more waits
+    int stage = 0;
+    uint32_t phase = 0;
+    bool dead = false;  // a wait ran out: no more waits
 
-    while (at < end) {
-        const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
-        const int hk = (int)((at - place) / t.groups);
-        const int first = (int)((at - place) % t.groups);
-        const int last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past
-
-        const int32_t* const table = p.c.table + t.b * p.c.table_stride;
-        // the table's entry for this lane's sub-block (lane % kSub) of a step, kUnread where none
-        // is needed; checked a step later, when it has arrived
-        auto page_of = [&](const Walk<D>& w) -> int {
-            const int j = w.j + 16 * (lane % G::kSub);
-            return w.x < last && j + 16 > w.lo(t) && j < w.hi(t) ? __ldg(table + (j >> p.c.page_shift)) : kUnread;
-        };
-        float pending = 0.f;  // this lane's scale of the step issued last, on its way
-        float* pending_at = nullptr;
-        auto issue = [&](const Walk<D>& w, int my_page) {
-            if (pending_at) *pending_at = pending;
-            pending_at = nullptr;
-            if (w.x >= last || dead) return;
-            if ((unsigned)my_page >= (unsigned)p.c.num_pages) {
-                if (my_page != kUnread) atomicOr(p.c.err, kErrBadPage);
-                my_page = -1;
-            }
-            const unsigned there = __ballot_sync(0xffffffffu, my_page >= 0) & ((1u << G::kSub) - 1);
-            if (lane < 2 * G::kSub) {  // lane: sub-block lane % kSub, of K or V
-                pending = kNoPage;
-                if (my_page >= 0)
-                    pending = __ldg((lane < G::kSub ? p.c.k.scale : p.c.v.scale) + (int64_t)my_page * p.c.Hk + hk);
-                pending_at = &sh.scales[warp][fill][lane];
-            }
-            const uint32_t bar = full_at + 8 * fill;
-            if (lane == 0) sm100::mbar_expect_tx(bar, 2 * G::kBox * __popc(there));
-            __syncwarp();
-            if (lane < G::kSub && my_page >= 0) {
-                const uint32_t dst = ring_at + fill * 2 * G::kSide + lane * G::kBox;
-                const int o = (w.j + 16 * lane) & page_mask;
-                sm100::tma_load_4d(dst, &k_map, bar, 0, o, hk, my_page);
-                sm100::tma_load_4d(dst + G::kSide, &v_map, bar, 0, o, hk, my_page);
-            }
-            fill = fill + 1 == kStages ? 0 : fill + 1;
-        };
-
+    while (part.open(p, rts)) {
+        const Tile& t = part.t;
         Query<T, D, R> q;
         State<D, R> st;
-        auto step = [&](const uint8_t* kd, const uint8_t* vd, const float* sc, int lo, int hi, int j0, auto all) {
+        auto step = [&](const uint8_t* kd, const uint8_t* vd, const float* ksc, const float* vsc, int lo, int hi, int j0, auto all) {
             constexpr bool full = decltype(all)::value;  // every row attends to every token of the step
             // S^T = K Q^T: e[k][sb][2 x + y]: row 8 k + 2 c + y, token 16 sb + 8 x + token(g)
             float e[R][G::kSub][4];
@@ -631,9 +706,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             float ks[G::kSub], lv[G::kSub], inv_vs[G::kSub];
 #pragma unroll
             for (int sb = 0; sb < G::kSub; ++sb) {
-                const float vs = sc[G::kSub + sb];
+                const float vs = vsc[sb];
                 const bool none = !full && vs < kMinScale;
-                ks[sb] = sc[sb];
+                ks[sb] = ksc[sb];
                 lv[sb] = none ? 0.f : sm100::lg2(vs);
                 inv_vs[sb] = none ? 1.f : __frcp_rn(vs);
             }
@@ -711,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             // O^T += V^T P^T
 #pragma unroll
             for (int sb = 0; sb < G::kSub; ++sb) {
-                if (!full && sc[G::kSub + sb] < kMinScale) continue;
+                if (!full && vsc[sb] < kMinScale) continue;
                 uint32_t pb[kParts][R][2];
 #pragma unroll
                 for (int k = 0; k < R; ++k)
@@ -749,43 +824,32 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                     }
             }
         };
-        Walk<D> ahead(t, first, warp), now(t, first, warp);
-        int page = page_of(ahead);
-        load_query<T, D, R>(p, t, hk, q);
+        load_query<T, D, R>(p, t, part.hk, q);
         st.clear();
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            issue(ahead, page);
-            ahead.next(t);
-            page = page_of(ahead);
-        }
-        for (; now.x < last; now.next(t)) {
-            if (!dead && !sm100::mbar_wait_bounded(full_at + 8 * stage, phase, kCacheWaitCycles)) {
-                dead = true;
-                if (lane == 0) atomicOr(p.c.err, kErrTimeout);
-            }
-            dead = __any_sync(0xffffffffu, dead);  // and every lane is done with the stage refilled next
-            issue(ahead, page);
-            ahead.next(t);
-            page = page_of(ahead);
-            const int lo = now.lo(t), hi = now.hi(t);
-            const uint8_t* kd = ring + stage * 2 * G::kSide;
+        Walk<D> now;
+        for (now.begin(t, part.first); now.x < part.last; now.next(t)) {
+            if (!dead && !sm100::mbar_wait_bounded(full_at + 8 * stage, phase, kCacheWaitCycles)) dead = true;
+            const int lo = now.lo(t), hi = now.hi(t), j0 = now.j + warp * G::kSub * 16;
+            const uint8_t* kd = ring + stage * (kWarps * 2 * G::kSide);
             const uint8_t* vd = kd + G::kSide;
-            const float* sc = &sh.scales[warp][stage][0];
+            const float *ksc = &sh.scales[stage][0][warp * G::kSub], *vsc = &sh.scales[stage][1][warp * G::kSub];
+            if (j0 + 16 * G::kSub > lo && j0 < hi) {
+                bool odd = false;  // a sub-block without a page or with a V scale of 0
+#pragma unroll
+                for (int sb = 0; sb < G::kSub; ++sb) odd |= vsc[sb] < kMinScale;
+                const int j_end = j0 + 16 * G::kSub;
+                const bool full = !odd && (now.x < t.na ? j_end <= t.full_a
+                                                        : j_end <= t.full_hi && (j0 >= t.full_lo || j_end <= t.full_a));
+                // two copies of the step, so that the common one carries no masks
+                if (full)
+                    step(kd, vd, ksc, vsc, lo, hi, j0, std::true_type{});
+                else
+                    step(kd, vd, ksc, vsc, lo, hi, j0, std::false_type{});
+            }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(empty_at + 8 * stage);
             stage = stage + 1 == kStages ? 0 : stage + 1;
             phase ^= stage == 0;
-            if (now.j + 16 * G::kSub <= lo || now.j >= hi) continue;
-            bool odd = false;  // a sub-block without a page or with a V scale of 0
-#pragma unroll
-            for (int sb = 0; sb < G::kSub; ++sb) odd |= sc[G::kSub + sb] < kMinScale;
-            const int j_end = now.j + 16 * G::kSub;
-            const bool full = !odd && (now.x < t.na ? j_end <= t.full_a
-                                                    : j_end <= t.full_hi && (now.j >= t.full_lo || j_end <= t.full_a));
-            // two copies of the step, so that the common one carries no masks
-            if (full)
-                step(kd, vd, sc, lo, hi, now.j, std::true_type{});
-            else
-                step(kd, vd, sc, lo, hi, now.j, std::false_type{});
         }
 #pragma unroll
         for (int k = 0; k < R; ++k)
@@ -795,30 +859,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 for (int z = 4; z < 32; z <<= 1) st.l[k][e] += __shfl_xor_sync(0xffffffffu, st.l[k][e], z);
         join_warps<D, R>(st, sh.ml, sh.join);
         if (warp == 0) {
-            if (first == 0 && last == t.groups)
-                write_rows<T, D, R>(p, t, hk, st);
+            if (part.first == 0 && part.last == t.groups)
+                write_rows<T, D, R>(p, t, part.hk, st);
             else  // slot 0: a segment that an earlier block began; slot 1: one that a later block goes on with
-                write_piece<D, R>(ws + ((int64_t)blockIdx.x * 2 + (first == 0)) * piece_floats<D, R>(), st, t.rows);
+                write_piece<D, R>(ws + ((int64_t)blockIdx.x * 2 + (part.first == 0)) * piece_floats<D, R>(), st, t.rows);
         }
-        at += last - first;
-        if (at >= place + (int64_t)t.groups * p.c.Hk) {
-            place += (int64_t)t.groups * p.c.Hk;
-            ++entry;
-        }
+        part.close(p);
     }
+    if (dead && lane == 0) atomicOr(p.c.err, kErrTimeout);
 }
 
 // Block x: segment x (entry x / Hk). The pieces of a segment that several blocks
 // worked on are added up: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
     __shared__ float tops[8 * R], sums_l[8 * R];
-    __shared__ int64_t sums[kThreads + 1];
+    __shared__ int64_t sums[kJoinThreads + 1];
     const int warp = threadIdx.x >> 5;
-    const Line line = line_total<D, R>(p, sums);
+    const Line line = line_total<D, R, kJoinThreads>(p, sums);
     const int blocks = line_blocks(line.total, grid), rts = row_tiles<R>(p);
     const int entry = blockIdx.x / p.c.Hk, hk = blockIdx.x % p.c.Hk;
-    const int per = (p.B * rts + kThreads - 1) / (kThreads);
+    const int per = (p.B * rts + kJoinThreads - 1) / (kJoinThreads);
     int64_t place = sums[entry / per];
     for (int e = entry / per * per; e < entry; ++e) place += make_tile<D, R>(p, e / rts, e % rts).groups;
     const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
@@ -836,7 +897,7 @@ __global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, c
     // the rows' references and sums: a warp every fourth row, its lanes over the pieces
     const int np = x1 - x0 + 1, lane = threadIdx.x & 31;
     auto piece = [&](int i) { return ws + ((int64_t)(x0 + i) * 2 + (i == 0)) * piece_floats<D, R>(); };
-    for (int row = warp; row < t.rows; row += kWarps) {
+    for (int row = warp; row < t.rows; row += kJoinThreads / 32) {
         float top = kNone, l = 0.f;
         for (int i = lane; i < np; i += 32) top = fmaxf(top, piece(i)[row]);
 #pragma unroll
@@ -853,7 +914,7 @@ __global__ void __launch_bounds__(kThreads) k_fwd_cache_join(CacheFwdParams p, c
     // a thread: 2 rows x 2 elements at a time
     constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32;
 #pragma unroll 1
-    for (int u = threadIdx.x; u < kUnits; u += kThreads) {
+    for (int u = threadIdx.x; u < kUnits; u += kJoinThreads) {
         const int k = u / (N * 32), i = u / 32 % N, g = (u & 31) >> 2, row = 8 * k + 2 * (u & 3);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < t.rows) {
@@ -919,7 +980,7 @@ cudaError_t side_map(CUtensorMap* map, const CacheSide& side, const CacheView& c
 
 template <typename T, int CODE, int D, int R>
 cudaError_t fwd_r(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t s) {
-    const int smem = (int)sizeof(Shared<D, R>) + kRingAlign - 16;
+    const int smem = (int)sizeof(Shared<D, R, stages<T, D, R>()>) + kRingAlign - 16;
     CUtensorMap k_map, v_map;
     cudaError_t e = side_map(&k_map, p.c.k, p.c, D);
     if (e == cudaSuccess) e = side_map(&v_map, p.c.v, p.c, D);
@@ -931,7 +992,7 @@ cudaError_t fwd_r(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t 
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)p.B * row_tiles<R>(p) * p.c.Hk));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = counted(s);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
