@@ -500,6 +500,7 @@ class Cache:
                 raise ValueError(f"cache {name}: unsupported dtype {t.dtype}")
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
         self.device = k.device
+        self.reals = {torch.bfloat16: SPATTN_BF16, torch.float32: SPATTN_F32}
         self.heads, self.page, self.d = k.shape[1:]
         self.batch, self.max_pages = page_table.shape
         self.desc = spattn_cache(_fill_desc(k, codes[k.dtype]), _fill_desc(v, codes[v.dtype]),
@@ -524,10 +525,9 @@ def _fill_desc(t, code: int) -> spattn_tensor:
 
 def _lens(t, name: str, cache: Cache) -> Optional[int]:
     """Address of an int32 [batch] tensor on the cache's device (or None)."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != cache.batch or not t.is_contiguous():
+    if t.dtype != cache.page_table.dtype or t.dim() != 1 or t.shape[0] != cache.batch or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [batch] tensor")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
@@ -537,26 +537,34 @@ def _lens(t, name: str, cache: Cache) -> Optional[int]:
 def _beside(t, name: str, cache: Cache) -> spattn_tensor:
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    return tensor_desc(t)
+    code = cache.reals.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError("spattn tensors are 4-D")
+    return _fill_desc(t, code)
 
 
-def _on(cache: Cache, stream):
-    """The stream of a cache call (default: the current stream of the cache's
-    device) and a context in which the cache's device is current."""
+def _call(fn, cache: Cache, stream, *args):
+    """fn(*args, stream) with the cache's device current; stream: by default that
+    device's current one."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream(cache.device)
-    return _stream(stream), torch.cuda.device(cache.device)
+    s = _stream(stream)
+    if torch.cuda.current_device() == cache.device.index:
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(cache.device):
+            _check(fn(*args, s))
 
 
 def spattn_cache_write(k, v, cache: Cache, start=None, length=None, stream=None) -> None:
     """Quantise the tokens k, v [batch, Hk, m, d] into the cache: token
     t < length[b] goes to place start[b] + t (int32 [batch] tensors; None: 0, and m)."""
     dk, dv = _beside(k, "k", cache), _beside(v, "v", cache)
-    st, ln = _lens(start, "start", cache), _lens(length, "length", cache)
-    s, on = _on(cache, stream)
-    with on:
-        _check(LIB.spattn_cache_write(ctypes.byref(dk), ctypes.byref(dv), ctypes.byref(cache.desc), st, ln, s))
+    _call(LIB.spattn_cache_write, cache, stream, dk, dv, cache.desc, _lens(start, "start", cache),
+          _lens(length, "length", cache))
 
 
 def spattn_cache_read(cache: Cache, m: int, dtype=None, start=None, length=None, k=None, v=None, stream=None):
@@ -571,10 +579,8 @@ def spattn_cache_read(cache: Cache, m: int, dtype=None, start=None, length=None,
     dk, dv = _beside(k, "k", cache), _beside(v, "v", cache)
     if k.shape[2] != m:
         raise ValueError(f"k holds {k.shape[2]} tokens, not {m}")
-    st, ln = _lens(start, "start", cache), _lens(length, "length", cache)
-    s, on = _on(cache, stream)
-    with on:
-        _check(LIB.spattn_cache_read(ctypes.byref(cache.desc), st, ln, ctypes.byref(dk), ctypes.byref(dv), s))
+    _call(LIB.spattn_cache_read, cache, stream, cache.desc, _lens(start, "start", cache),
+          _lens(length, "length", cache), dk, dv)
     return k, v
 
 
@@ -587,11 +593,8 @@ def spattn_fwd_cache(q, cache: Cache, seqlen, qlen=None, window: int = -1, n_glo
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
     out, lse = _outputs(q, out, lse, want_lse)
     dq, do = _beside(q, "q", cache), _beside(out, "out", cache)
-    sl, ql = _lens(seqlen, "seqlen", cache), _lens(qlen, "qlen", cache)
-    s, on = _on(cache, stream)
-    with on:
-        _check(LIB.spattn_fwd_cache(ctypes.byref(dq), ctypes.byref(cache.desc), sl, ql, window, n_global,
-                                    float(scale), ctypes.byref(do), _ptr(lse), s))
+    _call(LIB.spattn_fwd_cache, cache, stream, dq, cache.desc, _lens(seqlen, "seqlen", cache),
+          _lens(qlen, "qlen", cache), window, n_global, scale, do, _ptr(lse))
     return out, lse
 
 

@@ -1,15 +1,18 @@
 // Writing the 8-bit key/value cache, and reading it back.
 //
 // Write. Token t of the call goes to place start[b] + t of sequence b. One
-// thread block takes one page of one head, of K or of V, and reads that page's
-// new tokens once: they stay in registers between the two steps,
+// thread block (one warp, for a few tokens) takes one page of one head, of K or
+// of V, and reads that page's new tokens once; they stay in registers between
 //     a = max |x| (finite x),  s = max(a / qmax, the page's scale if it already holds older tokens),
 //     code = round(x / s), clipped to +-qmax,
 // and where s grew the older tokens' codes become round((c * s_old) / s). Both
 // quotients are IEEE fp32 quotients, so that the codes are a function of the
-// inputs alone. Bound: HBM (values in, codes out).
+// inputs alone; a division is only made where the product with 1 / s lies so near
+// a rounding border that it could round the other way. Bound: HBM (values in,
+// codes out).
 //
-// Read. One thread turns 16 codes (16 bytes) into 16 values. Bound: HBM.
+// Read. A thread turns 16 bytes' worth of values of several tokens, all loads
+// before the first use. Bound: HBM.
 #include "cache.cuh"
 
 namespace spattn {
@@ -40,10 +43,10 @@ struct Real<float> {
     }
 };
 
-// The code of x under scale s. A NaN becomes 0, an infinity the largest code of
-// its sign (the callers flag both).
+// The code of x under scale s, by division. A NaN becomes 0, an infinity the
+// largest code of its sign (the callers flag both).
 template <int CODE>
-__device__ __forceinline__ uint32_t make_code(float x, float s) {
+__device__ __forceinline__ uint32_t exact_code(float x, float s) {
     if (!(s > 0.f) || x != x) return 0u;
     float q = __fdiv_rn(x, s);
     q = fminf(fmaxf(q, -code_max<CODE>()), code_max<CODE>());
@@ -51,7 +54,74 @@ __device__ __forceinline__ uint32_t make_code(float x, float s) {
     return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// KV values of kVec codes in one store.
+// The codes of x[0..V) under scale s, and inv = 1 / s rounded. x inv is off from
+// the fp32 quotient by less than 4 units in the last place, so the two round to
+// the same code unless a border lies that near: for int8 a half, at most 2^-14
+// away (|q| < 128 has units of 2^-17); for e4m3 the bits below the code's three,
+// within 8 of a half. Quotients below e4m3's normal range, and all of a scale so
+// small that 1 / s loses bits, are divided too.
+template <int CODE, int V>
+__device__ __forceinline__ void make_codes(const float (&x)[V], float s, float inv, uint32_t (&w)[V / 4]) {
+    bool near = !(s > 1e-30f);
+    float q[V];
+#pragma unroll
+    for (int y = 0; y < V; ++y) {
+        q[y] = x[y] * inv;
+        near |= x[y] != x[y];
+        if constexpr (CODE == kCodeI8) {
+            near |= fabsf(fabsf(q[y] - rintf(q[y])) - 0.5f) < 6.103515625e-5f;
+        } else {
+            const uint32_t u = __float_as_uint(q[y]);
+            near |= (u - 0x7fff8u & 0xfffffu) <= 16u || (fabsf(q[y]) < 0.015625f && x[y] != 0.f);
+        }
+        q[y] = fminf(fmaxf(q[y], -code_max<CODE>()), code_max<CODE>());
+    }
+    if (near) {
+#pragma unroll
+        for (int y = 0; y < V / 4; ++y) w[y] = 0;
+#pragma unroll
+        for (int y = 0; y < V; ++y) w[y / 4] |= exact_code<CODE>(x[y], s) << (8 * (y % 4));
+        return;
+    }
+#pragma unroll
+    for (int y = 0; y < V / 4; ++y) {
+        if constexpr (CODE == kCodeI8) {
+            // 1.5 * 2^23 + q holds q's integer in its low bits, rounded to even
+            uint32_t b[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) b[z] = __float_as_uint(__fadd_rn(q[4 * y + z], 12582912.f));
+            w[y] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        } else {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * y], q[4 * y + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * y + 2], q[4 * y + 3]), __NV_SATFINITE, __NV_E4M3);
+            w[y] = lo | hi << 16;
+        }
+    }
+}
+
+// V codes as the fp32 products c * s.
+template <int CODE, int V>
+__device__ __forceinline__ void code_values(const uint32_t (&w)[V / 4], float s, float (&x)[V]) {
+#pragma unroll
+    for (int y = 0; y < V / 4; ++y) {
+        if constexpr (CODE == kCodeI8) {
+            const uint32_t u = w[y] ^ 0x80808080u;  // 2^23 + (c + 128)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                x[4 * y + z] = __fmul_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + z)) - 8388736.f, s);
+        } else {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[y] >> (16 * z)), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h));
+                x[4 * y + 2 * z] = __fmul_rn(f.x, s);
+                x[4 * y + 2 * z + 1] = __fmul_rn(f.y, s);
+            }
+        }
+    }
+}
+
+// V codes in one store or load.
 template <int V>
 __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[V / 4]) {
     if constexpr (V == 8) {
@@ -71,26 +141,29 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[V / 4
     }
 }
 
-// Threads of a block that share one page: page * D / kVec 16-byte vectors, NV a
-// thread.
-template <typename T, int CODE, int D, int NV>
-__global__ void __launch_bounds__(1024) k_cache_write(CacheView c, CacheRows r, int slots) {
+// W warps of a block share a page's D * page values as 16-byte vectors, NV a
+// thread; vectors behind the first NV (the page's older codes to renew, in the
+// one-warp form) are taken in further rounds. With W = 1 a block of four warps
+// takes four pages.
+template <typename T, int CODE, int D, int NV, bool kOneWarp>
+__global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView c, CacheRows r, int slots, int64_t items) {
     constexpr int V = Real<T>::kVec;
     constexpr int kRow = D / V;  // vectors a token
     __shared__ float s_amax[32];
-    int64_t x = blockIdx.x;
+    const int me = kOneWarp ? threadIdx.x & 31 : threadIdx.x, count = kOneWarp ? 32 : blockDim.x;
+    int64_t x = kOneWarp ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    if (x >= items) return;
     const int kv = (int)(x & 1);
-    x >>= 1;
-    const int h = (int)(x % c.Hk);
-    x /= c.Hk;
-    const int slot = (int)(x % slots);
-    const int b = (int)(x / slots);
+    uint32_t u = (uint32_t)(x >> 1);
+    const int h = (int)(u % (uint32_t)c.Hk);
+    u /= (uint32_t)c.Hk;
+    const int slot = (int)(u % (uint32_t)slots), b = (int)(u / (uint32_t)slots);
     const int64_t start = r.start ? r.start[b] : 0;
     int64_t end = r.length ? r.length[b] : r.m;
     end = start + (end < r.m ? end : r.m);
     const int64_t cap = cache_capacity(c);
     if (start < 0 || end > cap) {  // outside what the table can hold: the sequence is left out
-        if (end > start && threadIdx.x == 0) atomicOr(c.err, kErrBadPage);
+        if (end > start && me == 0) atomicOr(c.err, kErrBadPage);
         return;
     }
     const int page = 1 << c.page_shift;
@@ -99,25 +172,25 @@ __global__ void __launch_bounds__(1024) k_cache_write(CacheView c, CacheRows r, 
     const int64_t lo = p0 > start ? p0 : start;
     const int64_t hi = p0 + page < end ? p0 + page : end;
     const int pid = cache_page(c, b, p0);
-    if (pid < 0) return;
-    const CacheSide& side = kv ? c.v : c.k;
-    const T* src = static_cast<const T*>(kv ? r.v : r.k) + b * (kv ? r.v_sb : r.k_sb) + h * (kv ? r.v_sh : r.k_sh);
+    const int older = (int)(lo - p0), fresh = (int)(hi - lo);  // places [0, older), then `fresh` new ones
+    const T* src = static_cast<const T*>(kv ? r.v : r.k) + b * (kv ? r.v_sb : r.k_sb) + h * (kv ? r.v_sh : r.k_sh) +
+                   (lo - start) * (kv ? r.v_sn : r.k_sn);
     const int64_t s_n = kv ? r.v_sn : r.k_sn;
-    uint8_t* dst = side.codes + pid * side.s_p + h * side.s_h;
-    float* scale = side.scale + (int64_t)pid * c.Hk + h;
-    const int older = (int)(lo - p0), fresh_end = (int)(hi - p0);  // places [older, fresh_end) are new
+    const CacheSide& side = kv ? c.v : c.k;
 
     uint4 w[NV];
     float amax = 0.f;
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = i * blockDim.x + threadIdx.x;
-        const int o = e / kRow, at = (e % kRow) * V;
+        const int e = i * count + me;
         w[i] = make_uint4(0, 0, 0, 0);
-        if (o >= older && o < fresh_end)
-            w[i] = *reinterpret_cast<const uint4*>(src + (p0 + o - start) * s_n + at);
+        if (e < fresh * kRow) w[i] = __ldg(reinterpret_cast<const uint4*>(src + (e / kRow) * s_n + (e % kRow) * V));
     }
+    if (pid < 0) return;
+    uint8_t* const dst = side.codes + pid * side.s_p + h * side.s_h;
+    float* const scale = side.scale + (int64_t)pid * c.Hk + h;
+    const float before = older > 0 ? *scale : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         float f[V];
@@ -133,122 +206,145 @@ __global__ void __launch_bounds__(1024) k_cache_write(CacheView c, CacheRows r, 
     if (odd) atomicOr(c.err, kErrNonFinite);
 #pragma unroll
     for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-    if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
-    const float before = older > 0 ? *scale : 0.f;
-    __syncthreads();
-    for (int y = 0; y < (int)(blockDim.x >> 5); ++y) amax = fmaxf(amax, s_amax[y]);
-    const float fresh = __fdiv_rn(amax, code_max<CODE>());
-    const bool grown = fresh > before;
-    const float s = grown ? fresh : before;
-    if (threadIdx.x == 0 && (grown || older == 0)) *scale = s;  // every thread has read it before the barrier
+    if constexpr (!kOneWarp) {
+        if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
+        __syncthreads();  // and every thread has read the scale
+        for (int y = 0; y < (int)(blockDim.x >> 5); ++y) amax = fmaxf(amax, s_amax[y]);
+    }
+    const float s_new = __fdiv_rn(amax, code_max<CODE>());
+    const bool grown = s_new > before;
+    const float s = grown ? s_new : before, inv = __frcp_rn(s);
+    if (me == 0 && (grown || older == 0)) *scale = s;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = i * blockDim.x + threadIdx.x;
-        const int o = e / kRow, at = (e % kRow) * V;
-        uint8_t* p = dst + o * side.s_t + at;
+        const int e = i * count + me;
+        if (e >= fresh * kRow) continue;
         float f[V];
-        if (o >= older && o < fresh_end) {
-            Real<T>::unpack(w[i], f);
-        } else if (o < older && grown) {
-            uint32_t u[V / 4];
-            load_codes<V>(p, u);
-#pragma unroll
-            for (int y = 0; y < V; ++y)
-                f[y] = __fmul_rn(code_value<CODE>((u[y / 4] >> (8 * (y % 4))) & 0xffu), before);
-        } else {
-            continue;
+        uint32_t u8[V / 4];
+        Real<T>::unpack(w[i], f);
+        make_codes<CODE, V>(f, s, inv, u8);
+        store_codes<V>(dst + (older + e / kRow) * side.s_t + (e % kRow) * V, u8);
+    }
+    if (older > 0 && grown) {
+        for (int e = me; e < older * kRow; e += count) {
+            uint8_t* const at = dst + (e / kRow) * side.s_t + (e % kRow) * V;
+            float f[V];
+            uint32_t u8[V / 4];
+            load_codes<V>(at, u8);
+            code_values<CODE, V>(u8, before, f);
+            make_codes<CODE, V>(f, s, inv, u8);
+            store_codes<V>(at, u8);
         }
-        uint32_t u[V / 4];
-#pragma unroll
-        for (int y = 0; y < V / 4; ++y) u[y] = 0;
-#pragma unroll
-        for (int y = 0; y < V; ++y) u[y / 4] |= make_code<CODE>(f[y], s) << (8 * (y % 4));
-        store_codes<V>(p, u);
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_values(T* p, const float (&f)[16]);
-template <>
-__device__ __forceinline__ void store_values<__nv_bfloat16>(__nv_bfloat16* p, const float (&f)[16]) {
-    uint32_t u[8];
+// One 16-byte vector of V values.
+template <typename T, int V>
+__device__ __forceinline__ uint4 pack_values(const float (&f)[V]) {
+    uint32_t u[4];
+    if constexpr (V == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
     }
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-}
-template <>
-__device__ __forceinline__ void store_values<float>(float* p, const float (&f)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// A block: 256 / (D / 16) tokens of one (b, h), of K (z = 0) or V (z = 1).
+// A block: kTokens tokens of one (b, h), of K (z = 0) or V (z = 1); a thread: one
+// vector of kUnroll of them.
 template <typename T, int CODE, int D>
-__global__ void __launch_bounds__(256) k_cache_read(CacheView c, CacheRows r) {
-    constexpr int kRow = D / 16, kTokens = 256 / kRow;
+struct ReadGeo {
+    static constexpr int kThreads = 128, kUnroll = 8;
+    static constexpr int kRow = D / Real<T>::kVec, kStep = kThreads / kRow, kTokens = kStep * kUnroll;
+};
+template <typename T, int CODE, int D>
+__global__ void __launch_bounds__(128) k_cache_read(CacheView c, CacheRows r) {
+    using G = ReadGeo<T, CODE, D>;
+    constexpr int V = Real<T>::kVec, U = G::kUnroll;
     const int h = (int)(blockIdx.x % c.Hk), b = (int)(blockIdx.x / c.Hk);
     const bool kv = blockIdx.z != 0;
     const CacheSide& side = kv ? c.v : c.k;
     const int64_t start = r.start ? r.start[b] : 0;
-    const int64_t asked = r.length ? r.length[b] : r.m;
+    int64_t asked = r.length ? r.length[b] : r.m;
     const int64_t cap = cache_capacity(c);
     T* dst = static_cast<T*>(kv ? r.v : r.k) + b * (kv ? r.v_sb : r.k_sb) + h * (kv ? r.v_sh : r.k_sh);
     const int64_t s_n = kv ? r.v_sn : r.k_sn;
-    const int at = (threadIdx.x % kRow) * 16;
-    for (int64_t t = (int64_t)blockIdx.y * kTokens + threadIdx.x / kRow; t < r.m; t += (int64_t)gridDim.y * kTokens) {
-        float f[16];
+    const int at = (threadIdx.x % G::kRow) * V;
+    const uint8_t* codes = side.codes + h * side.s_h + at;
+    const int32_t* table = c.table + b * c.table_stride;
+    for (int64_t t0 = (int64_t)blockIdx.y * G::kTokens + threadIdx.x / G::kRow; t0 < r.m;
+         t0 += (int64_t)gridDim.y * G::kTokens) {
+        int pid[U];
+        float s[U];
+        uint32_t w[U][V / 4];
 #pragma unroll
-        for (int y = 0; y < 16; ++y) f[y] = 0.f;
-        const int64_t j = start + t;
-        if (t < asked) {
-            int pid = -1;
-            if (j >= 0 && j < cap)
-                pid = cache_page(c, b, j);
-            else
+        for (int i = 0; i < U; ++i) {
+            const int64_t t = t0 + i * G::kStep, j = start + t;
+            const bool in = t < asked && t < r.m, held = j >= 0 && j < cap;
+            pid[i] = -1;
+            if (in && held) pid[i] = __ldg(table + (j >> c.page_shift));
+            if (in && (!held || (unsigned)pid[i] >= (unsigned)c.num_pages)) {
                 atomicOr(c.err, kErrBadPage);
-            if (pid >= 0) {
-                const int o = (int)(j & ((1 << c.page_shift) - 1));
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(side.codes + pid * side.s_p + h * side.s_h +
-                                                                     o * side.s_t + at));
-                const float s = __ldg(side.scale + (int64_t)pid * c.Hk + h);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int y = 0; y < 16; ++y)
-                    f[y] = __fmul_rn(code_value<CODE>((u[y / 4] >> (8 * (y % 4))) & 0xffu), s);
+                pid[i] = -1;
             }
         }
-        store_values<T>(dst + t * s_n + at, f);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int y = 0; y < V / 4; ++y) w[i][y] = 0;
+            s[i] = 0.f;
+            if (pid[i] >= 0) {
+                const int o = (int)((start + t0 + i * G::kStep) & ((1 << c.page_shift) - 1));
+                load_codes<V>(codes + pid[i] * side.s_p + o * side.s_t, w[i]);
+                s[i] = __ldg(side.scale + (int64_t)pid[i] * c.Hk + h);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t t = t0 + i * G::kStep;
+            if (t >= r.m) break;
+            float f[V];
+            code_values<CODE, V>(w[i], s[i], f);
+            if (pid[i] < 0) {  // zeros, not 0 * 0 of some sign
+#pragma unroll
+                for (int y = 0; y < V; ++y) f[y] = 0.f;
+            }
+            *reinterpret_cast<uint4*>(dst + t * s_n + at) = pack_values<T, V>(f);
+        }
     }
 }
 
 template <typename T, int CODE, int D>
 cudaError_t write_d(const CacheView& c, const CacheRows& r, cudaStream_t s) {
+    constexpr int V = Real<T>::kVec;
     const int page = 1 << c.page_shift;
     const int slots = (int)(((int64_t)r.m + page - 2) / page + 1);
-    const int vecs = page * D / Real<T>::kVec;
-    const int threads = vecs / 4 < 32 ? 32 : vecs / 4 > 1024 ? 1024 : vecs / 4;
-    const int64_t blocks = (int64_t)c.B * slots * c.Hk * 2;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    switch (vecs / threads) {
-        case 2: k_cache_write<T, CODE, D, 2><<<(unsigned)blocks, threads, 0, counted(s)>>>(c, r, slots); break;
-        case 4: k_cache_write<T, CODE, D, 4><<<(unsigned)blocks, threads, 0, counted(s)>>>(c, r, slots); break;
-        case 8: k_cache_write<T, CODE, D, 8><<<(unsigned)blocks, threads, 0, counted(s)>>>(c, r, slots); break;
-        default: return cudaErrorInvalidConfiguration;
+    const int64_t items = (int64_t)c.B * slots * c.Hk * 2;
+    // a warp holds four vectors a lane: enough for all new values of a page when the call brings few tokens
+    if ((int64_t)(r.m < page ? r.m : page) * D / V <= 128) {
+        k_cache_write<T, CODE, D, 4, true><<<(unsigned)((items + 3) / 4), 128, 0, counted(s)>>>(c, r, slots, items);
+        return cudaGetLastError();
     }
+    const int vecs = page * D / V;  // > 128
+    const int threads = vecs / 4 > 1024 ? 1024 : vecs / 4;
+    if (vecs / threads == 4)
+        k_cache_write<T, CODE, D, 4, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items);
+    else  // 8: fp32 pages of 256 tokens of 128
+        k_cache_write<T, CODE, D, 8, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items);
     return cudaGetLastError();
 }
 
 template <typename T, int CODE, int D>
 cudaError_t read_d(const CacheView& c, const CacheRows& r, cudaStream_t s) {
-    constexpr int kTokens = 256 / (D / 16);
-    const int64_t y = ((int64_t)r.m + kTokens - 1) / kTokens;
+    using G = ReadGeo<T, CODE, D>;
+    const int64_t y = ((int64_t)r.m + G::kTokens - 1) / G::kTokens;
     const dim3 grid((unsigned)(c.B * c.Hk), (unsigned)(y < 65535 ? y : 65535), 2);
-    k_cache_read<T, CODE, D><<<grid, 256, 0, counted(s)>>>(c, r);
+    k_cache_read<T, CODE, D><<<grid, G::kThreads, 0, counted(s)>>>(c, r);
     return cudaGetLastError();
 }
 

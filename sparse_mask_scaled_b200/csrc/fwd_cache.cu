@@ -187,9 +187,25 @@ __device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[NT + 1]
     *entry = e;
     *first = place;
 }
-// Blocks that take part, and the first place of block x of them.
-__device__ __forceinline__ int line_blocks(int64_t total, int grid) { return total < grid ? (int)total : grid; }
-__device__ __forceinline__ int64_t line_start(int64_t total, int blocks, int x) { return total * x / blocks; }
+// a / b for a >= 0, b > 0, in 32 bits where they fit (a fraction of the time).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// The line's blocks: the first `longer` of `blocks` hold share + 1 places, the others `share`.
+struct Shares {
+    int blocks;
+    int64_t share, longer;
+    __device__ __forceinline__ Shares(int64_t total, int grid) {
+        blocks = total < grid ? (int)total : grid;
+        share = quotient(total, blocks);
+        longer = total - share * blocks;
+    }
+    __device__ __forceinline__ int64_t start(int x) const { return share * x + (x < longer ? x : longer); }
+    __device__ __forceinline__ int block_of(int64_t place) const {
+        const int64_t cut = (share + 1) * longer;
+        return (int)(place < cut ? quotient(place, share + 1) : longer + quotient(place - cut, share));
+    }
+};
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -525,8 +541,8 @@ struct Part {
     __device__ __forceinline__ bool open(const CacheFwdParams& p, int rts) {  // the segment that holds `at`
         if (at >= end) return false;
         t = make_tile<D, R>(p, entry / rts, entry % rts);
-        hk = (int)((at - place) / t.groups);
-        first = (int)((at - place) % t.groups);
+        hk = (int)quotient(at - place, t.groups);
+        first = (int)(at - place - (int64_t)hk * t.groups);
         last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past
         return true;
     }
@@ -643,12 +659,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
     }
 
     const Line line = line_total<D, R, kThreads>(p, sh.sums);  // (with barriers)
-    const int blocks = line_blocks(line.total, (int)gridDim.x);
-    if ((int)blockIdx.x >= blocks) return;
+    const Shares shares(line.total, (int)gridDim.x);
+    if ((int)blockIdx.x >= shares.blocks) return;
     const int rts = row_tiles<R>(p);
     Part<D, R> part;
-    part.at = line_start(line.total, blocks, blockIdx.x);
-    part.end = line_start(line.total, blocks, blockIdx.x + 1);
+    part.at = shares.start(blockIdx.x);
+    part.end = shares.start(blockIdx.x + 1);
     line_find<D, R, kThreads>(p, sh.sums, part.at, &part.entry, &part.place);
     if (warp == kWarps) {
         produce<D, R, kStages>(k_map, v_map, p, sh, part, rts);
@@ -877,21 +893,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_fwd_cache_join(CacheFwdParams 
     __shared__ int64_t sums[kJoinThreads + 1];
     const int warp = threadIdx.x >> 5;
     const Line line = line_total<D, R, kJoinThreads>(p, sums);
-    const int blocks = line_blocks(line.total, grid), rts = row_tiles<R>(p);
+    const Shares shares(line.total, grid);
+    const int rts = row_tiles<R>(p);
     const int entry = blockIdx.x / p.c.Hk, hk = blockIdx.x % p.c.Hk;
     const int per = (p.B * rts + kJoinThreads - 1) / (kJoinThreads);
     int64_t place = sums[entry / per];
     for (int e = entry / per * per; e < entry; ++e) place += make_tile<D, R>(p, e / rts, e % rts).groups;
     const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
     const int64_t s0 = place * p.c.Hk + (int64_t)hk * t.groups, s1 = s0 + t.groups - 1;
-    // the block that holds place s: the last x with total x / blocks <= s
-    auto block_of = [&](int64_t s) {
-        int x = (int)((s * blocks + blocks - 1) / line.total);
-        while (x > 0 && line_start(line.total, blocks, x) > s) --x;
-        while (x + 1 < blocks && line_start(line.total, blocks, x + 1) <= s) ++x;
-        return x;
-    };
-    const int x0 = block_of(s0), x1 = block_of(s1);
+    const int x0 = shares.block_of(s0), x1 = shares.block_of(s1);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // every block, so that this kernel ends after the first
     if (x0 == x1) return;
     // the rows' references and sums: a warp every fourth row, its lanes over the pieces
