@@ -549,9 +549,10 @@ def _call(fn, cache: Cache, stream, *args):
     """fn(*args, stream) with the cache's device current; stream: by default that
     device's current one."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    s = _stream(stream)
+    if stream is None:  # a token's step is a few microseconds: no Stream object for its address
+        s = torch._C._cuda_getCurrentRawStream(cache.device.index)
+    else:
+        s = _stream(stream)
     if torch.cuda.current_device() == cache.device.index:
         _check(fn(*args, s))
     else:

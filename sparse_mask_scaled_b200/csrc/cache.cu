@@ -31,6 +31,19 @@ struct Real<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
     }
+    // The largest magnitude (as bits, so that a NaN counts as more than infinity).
+    template <int N>
+    static __device__ __forceinline__ float top(const uint4 (&w)[N]) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            t = __vmaxu2(t, w[i].x & 0x7fff7fffu);
+            t = __vmaxu2(t, w[i].y & 0x7fff7fffu);
+            t = __vmaxu2(t, w[i].z & 0x7fff7fffu);
+            t = __vmaxu2(t, w[i].w & 0x7fff7fffu);
+        }
+        return __uint_as_float(max(t >> 16, t & 0xffffu) << 16);
+    }
 };
 template <>
 struct Real<float> {
@@ -40,6 +53,14 @@ struct Real<float> {
         x[1] = __uint_as_float(w.y);
         x[2] = __uint_as_float(w.z);
         x[3] = __uint_as_float(w.w);
+    }
+    template <int N>
+    static __device__ __forceinline__ float top(const uint4 (&w)[N]) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            t = max(max(t, max(w[i].x & 0x7fffffffu, w[i].y & 0x7fffffffu)), max(w[i].z & 0x7fffffffu, w[i].w & 0x7fffffffu));
+        return __uint_as_float(t);
     }
 };
 
@@ -54,48 +75,52 @@ __device__ __forceinline__ uint32_t exact_code(float x, float s) {
     return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// The codes of x[0..V) under scale s, and inv = 1 / s rounded. x inv is off from
-// the fp32 quotient by less than 4 units in the last place, so the two round to
-// the same code unless a border lies that near: for int8 a half, at most 2^-14
-// away (|q| < 128 has units of 2^-17); for e4m3 the bits below the code's three,
-// within 8 of a half. Quotients below e4m3's normal range, and all of a scale so
-// small that 1 / s loses bits, are divided too.
+// The codes of finite x[0..V), |x| <= qmax s (1 + 2^-23), and inv = 1 / s rounded.
+// x inv is off from the fp32 quotient by less than 4 units in the last place, so
+// the two round to the same code unless a border lies that near: for int8 a half,
+// at most 2^-14 away (|q| < 128 has units of 2^-17); for e4m3 the bits below the
+// code's three, within 8 of a half. Quotients below e4m3's normal range are
+// divided too, and so is everything where `divide` says so.
 template <int CODE, int V>
-__device__ __forceinline__ void make_codes(const float (&x)[V], float s, float inv, uint32_t (&w)[V / 4]) {
-    bool near = !(s > 1e-30f);
+__device__ __forceinline__ void make_codes(const float (&x)[V], float s, float inv, bool divide, uint32_t (&w)[V / 4]) {
     float q[V];
+    if constexpr (CODE == kCodeI8) {
+        float far = 0.f, r[V];
 #pragma unroll
-    for (int y = 0; y < V; ++y) {
-        q[y] = x[y] * inv;
-        near |= x[y] != x[y];
-        if constexpr (CODE == kCodeI8) {
-            near |= fabsf(fabsf(q[y] - rintf(q[y])) - 0.5f) < 6.103515625e-5f;
-        } else {
-            const uint32_t u = __float_as_uint(q[y]);
-            near |= (u - 0x7fff8u & 0xfffffu) <= 16u || (fabsf(q[y]) < 0.015625f && x[y] != 0.f);
+        for (int y = 0; y < V; ++y) {
+            q[y] = __fmul_rn(x[y], inv);
+            r[y] = __fadd_rn(q[y], 12582912.f);  // 1.5 * 2^23: q's integer, ties to even, in the low bits
+            far = fmaxf(far, fabsf(q[y] - __fadd_rn(r[y], -12582912.f)));
         }
-        q[y] = fminf(fmaxf(q[y], -code_max<CODE>()), code_max<CODE>());
-    }
-    if (near) {
+        divide |= far > 0.5f - 6.103515625e-5f;
 #pragma unroll
-        for (int y = 0; y < V / 4; ++y) w[y] = 0;
-#pragma unroll
-        for (int y = 0; y < V; ++y) w[y / 4] |= exact_code<CODE>(x[y], s) << (8 * (y % 4));
-        return;
-    }
-#pragma unroll
-    for (int y = 0; y < V / 4; ++y) {
-        if constexpr (CODE == kCodeI8) {
-            // 1.5 * 2^23 + q holds q's integer in its low bits, rounded to even
-            uint32_t b[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) b[z] = __float_as_uint(__fadd_rn(q[4 * y + z], 12582912.f));
+        for (int y = 0; y < V / 4; ++y) {
+            const uint32_t b[4] = {__float_as_uint(r[4 * y]), __float_as_uint(r[4 * y + 1]), __float_as_uint(r[4 * y + 2]),
+                                   __float_as_uint(r[4 * y + 3])};
             w[y] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        } else {
+        }
+    } else {
+        uint32_t gap = ~0u;
+        float low = INFINITY;
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+            q[y] = __fmul_rn(x[y], inv);
+            gap = min(gap, (__float_as_uint(q[y]) - 0x7fff8u) & 0xfffffu);
+            low = fminf(low, fabsf(q[y]));
+        }
+        divide |= gap <= 16u || low < 0.015625f;
+#pragma unroll
+        for (int y = 0; y < V / 4; ++y) {
             const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * y], q[4 * y + 1]), __NV_SATFINITE, __NV_E4M3);
             const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * y + 2], q[4 * y + 3]), __NV_SATFINITE, __NV_E4M3);
             w[y] = lo | hi << 16;
         }
+    }
+    if (divide) {
+#pragma unroll
+        for (int y = 0; y < V / 4; ++y) w[y] = 0;
+#pragma unroll
+        for (int y = 0; y < V; ++y) w[y / 4] |= exact_code<CODE>(x[y], s) << (8 * (y % 4));
     }
 }
 
@@ -146,7 +171,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[V / 4
 // one-warp form) are taken in further rounds. With W = 1 a block of four warps
 // takes four pages.
 template <typename T, int CODE, int D, int NV, bool kOneWarp>
-__global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView c, CacheRows r, int slots, int64_t items) {
+__global__ void __launch_bounds__(kOneWarp ? 128 : 1024, kOneWarp ? 8 : NV <= 2 ? 2 : 1)
+    k_cache_write(CacheView c, CacheRows r, int slots, int64_t items) {
     constexpr int V = Real<T>::kVec;
     constexpr int kRow = D / V;  // vectors a token
     __shared__ float s_amax[32];
@@ -179,8 +205,6 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView
     const CacheSide& side = kv ? c.v : c.k;
 
     uint4 w[NV];
-    float amax = 0.f;
-    bool odd = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = i * count + me;
@@ -191,19 +215,19 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView
     uint8_t* const dst = side.codes + pid * side.s_p + h * side.s_h;
     float* const scale = side.scale + (int64_t)pid * c.Hk + h;
     const float before = older > 0 ? *scale : 0.f;
+    float amax = Real<T>::template top<NV>(w);
+    const bool odd = !(amax < INFINITY);
+    if (odd) {  // the largest of the finite ones
+        atomicOr(c.err, kErrNonFinite);
+        amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float f[V];
-        Real<T>::unpack(w[i], f);
+        for (int i = 0; i < NV; ++i) {
+            float f[V];
+            Real<T>::unpack(w[i], f);
 #pragma unroll
-        for (int y = 0; y < V; ++y) {
-            const float a = fabsf(f[y]);
-            const bool finite = a < INFINITY;
-            odd |= !finite;
-            amax = fmaxf(amax, finite ? a : 0.f);
+            for (int y = 0; y < V; ++y) amax = fmaxf(amax, fabsf(f[y]) < INFINITY ? fabsf(f[y]) : 0.f);
         }
     }
-    if (odd) atomicOr(c.err, kErrNonFinite);
 #pragma unroll
     for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
     if constexpr (!kOneWarp) {
@@ -214,6 +238,7 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView
     const float s_new = __fdiv_rn(amax, code_max<CODE>());
     const bool grown = s_new > before;
     const float s = grown ? s_new : before, inv = __frcp_rn(s);
+    const bool divide = odd || !(s > 1e-30f);  // below, 1 / s or the products lose bits
     if (me == 0 && (grown || older == 0)) *scale = s;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -222,7 +247,7 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView
         float f[V];
         uint32_t u8[V / 4];
         Real<T>::unpack(w[i], f);
-        make_codes<CODE, V>(f, s, inv, u8);
+        make_codes<CODE, V>(f, s, inv, divide, u8);
         store_codes<V>(dst + (older + e / kRow) * side.s_t + (e % kRow) * V, u8);
     }
     if (older > 0 && grown) {
@@ -232,7 +257,7 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024) k_cache_write(CacheView
             uint32_t u8[V / 4];
             load_codes<V>(at, u8);
             code_values<CODE, V>(u8, before, f);
-            make_codes<CODE, V>(f, s, inv, u8);
+            make_codes<CODE, V>(f, s, inv, true, u8);
             store_codes<V>(at, u8);
         }
     }
@@ -330,12 +355,14 @@ cudaError_t write_d(const CacheView& c, const CacheRows& r, cudaStream_t s) {
         k_cache_write<T, CODE, D, 4, true><<<(unsigned)((items + 3) / 4), 128, 0, counted(s)>>>(c, r, slots, items);
         return cudaGetLastError();
     }
+    // two vectors a thread, so that 2048 threads fit an SM; more only for the largest pages
     const int vecs = page * D / V;  // > 128
-    const int threads = vecs / 4 > 1024 ? 1024 : vecs / 4;
-    if (vecs / threads == 4)
-        k_cache_write<T, CODE, D, 4, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items);
-    else  // 8: fp32 pages of 256 tokens of 128
-        k_cache_write<T, CODE, D, 8, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items);
+    const int threads = vecs / 2 > 1024 ? 1024 : vecs / 2;
+    switch (vecs / threads) {
+        case 2: k_cache_write<T, CODE, D, 2, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items); break;
+        case 4: k_cache_write<T, CODE, D, 4, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items); break;
+        default: k_cache_write<T, CODE, D, 8, false><<<(unsigned)items, threads, 0, counted(s)>>>(c, r, slots, items); break;
+    }
     return cudaGetLastError();
 }
 

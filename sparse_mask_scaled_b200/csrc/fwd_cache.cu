@@ -81,6 +81,11 @@ struct Geo {
         return o * D + (at ^ (16 * x));
     }
 };
+// What a block leaves for the joining kernel: the segment that it began and later
+// blocks went on with, if there is one (more = how many).
+struct Begun {
+    int more, b, first_row, rows, hk, pad[3];
+};
 // Floats of a stored piece: m and l of the 8 R rows, then O.
 template <int D, int R>
 constexpr int piece_floats() {
@@ -658,6 +663,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
         sm100::prefetch_tensormap(&v_map);
     }
 
+    Begun* const begun = reinterpret_cast<Begun*>(ws);
+    float* const pieces = ws + (int64_t)gridDim.x * (sizeof(Begun) / 4);
+    if (threadIdx.x == 0) begun[blockIdx.x].more = 0;
     const Line line = line_total<D, R, kThreads>(p, sh.sums);  // (with barriers)
     const Shares shares(line.total, (int)gridDim.x);
     if ((int)blockIdx.x >= shares.blocks) return;
@@ -877,85 +885,95 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
         if (warp == 0) {
             if (part.first == 0 && part.last == t.groups)
                 write_rows<T, D, R>(p, t, part.hk, st);
-            else  // slot 0: a segment that an earlier block began; slot 1: one that a later block goes on with
-                write_piece<D, R>(ws + ((int64_t)blockIdx.x * 2 + (part.first == 0)) * piece_floats<D, R>(), st, t.rows);
+            else  // slot 0: a segment that an earlier block began; slot 1: one that later blocks go on with
+                write_piece<D, R>(pieces + ((int64_t)blockIdx.x * 2 + (part.first == 0)) * piece_floats<D, R>(), st, t.rows);
+            if (part.first == 0 && part.last < t.groups && lane == 0) {
+                const int64_t end = part.place + (int64_t)(part.hk + 1) * t.groups - 1;
+                begun[blockIdx.x] = Begun{shares.block_of(end) - (int)blockIdx.x, t.b, t.first_row, t.rows, part.hk, {}};
+            }
         }
         part.close(p);
     }
     if (dead && lane == 0) atomicOr(p.c.err, kErrTimeout);
 }
 
-// Block x: segment x (entry x / Hk). The pieces of a segment that several blocks
-// worked on are added up: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// Block x: the segment that block x of the other kernel began and others went on
+// with: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its pieces.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
-    __shared__ float tops[8 * R], sums_l[8 * R];
-    __shared__ int64_t sums[kJoinThreads + 1];
-    const int warp = threadIdx.x >> 5;
-    const Line line = line_total<D, R, kJoinThreads>(p, sums);
-    const Shares shares(line.total, grid);
-    const int rts = row_tiles<R>(p);
-    const int entry = blockIdx.x / p.c.Hk, hk = blockIdx.x % p.c.Hk;
-    const int per = (p.B * rts + kJoinThreads - 1) / (kJoinThreads);
-    int64_t place = sums[entry / per];
-    for (int e = entry / per * per; e < entry; ++e) place += make_tile<D, R>(p, e / rts, e % rts).groups;
-    const Tile t = make_tile<D, R>(p, entry / rts, entry % rts);
-    const int64_t s0 = place * p.c.Hk + (int64_t)hk * t.groups, s1 = s0 + t.groups - 1;
-    const int x0 = shares.block_of(s0), x1 = shares.block_of(s1);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // every block, so that this kernel ends after the first
-    if (x0 == x1) return;
+    constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32, kBatch = 32;
+    __shared__ float tops[8 * R], sums[8 * R], weights[kBatch][8 * R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Begun t = reinterpret_cast<const Begun*>(ws)[blockIdx.x];
+    if (t.more <= 0) return;
+    const int np = t.more + 1;
+    const float* const pieces = ws + (int64_t)grid * (sizeof(Begun) / 4);
+    auto piece = [&](int i) { return pieces + ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * piece_floats<D, R>(); };
     // the rows' references and sums: a warp every fourth row, its lanes over the pieces
-    const int np = x1 - x0 + 1, lane = threadIdx.x & 31;
-    auto piece = [&](int i) { return ws + ((int64_t)(x0 + i) * 2 + (i == 0)) * piece_floats<D, R>(); };
-    for (int row = warp; row < t.rows; row += kJoinThreads / 32) {
+    for (int row = warp; row < 8 * R; row += kJoinThreads / 32) {
         float top = kNone, l = 0.f;
-        for (int i = lane; i < np; i += 32) top = fmaxf(top, piece(i)[row]);
+        if (row < t.rows) {
+            for (int i = lane; i < np; i += 32) top = fmaxf(top, piece(i)[row]);
 #pragma unroll
-        for (int z = 1; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-        for (int i = lane; i < np; i += 32) l += ex2(piece(i)[row] - top) * piece(i)[8 * R + row];
+            for (int z = 1; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+            for (int i = lane; i < np; i += 32) l += ex2(piece(i)[row] - top) * piece(i)[8 * R + row];
 #pragma unroll
-        for (int z = 1; z < 32; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+            for (int z = 1; z < 32; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
+        }
         if (lane == 0) {
             tops[row] = top;
-            sums_l[row] = l;
+            sums[row] = l;
         }
     }
-    __syncthreads();
-    // a thread: 2 rows x 2 elements at a time
-    constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32;
-#pragma unroll 1
-    for (int u = threadIdx.x; u < kUnits; u += kJoinThreads) {
-        const int k = u / (N * 32), i = u / 32 % N, g = (u & 31) >> 2, row = 8 * k + 2 * (u & 3);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < t.rows) {
-            const float top0 = tops[row], top1 = row + 1 < t.rows ? tops[row + 1] : 0.f;
-#pragma unroll 4
-            for (int x = 0; x < np; ++x) {
-                const float* src = piece(x);
-                const float2 m = *reinterpret_cast<const float2*>(src + row);
-                const float4 v = reinterpret_cast<const float4*>(src + 16 * R)[u];
-                const float w0 = ex2(m.x - top0), w1 = row + 1 < t.rows ? ex2(m.y - top1) : 0.f;
-                o.x += v.x * w0;
-                o.y += v.y * w1;
-                o.z += v.z * w0;
-                o.w += v.w * w1;
+    // a thread: 2 rows x 2 elements of kUnits / kJoinThreads places
+    constexpr int kMine = kUnits / kJoinThreads > 0 ? kUnits / kJoinThreads : 1;
+    float4 o[kMine];
+#pragma unroll
+    for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < np; i0 += kBatch) {
+        const int n = np - i0 < kBatch ? np - i0 : kBatch;
+        __syncthreads();
+        for (int x = threadIdx.x; x < n * 8 * R; x += kJoinThreads) {
+            const int row = x % (8 * R);
+            weights[x / (8 * R)][row] = row < t.rows ? ex2(piece(i0 + x / (8 * R))[row] - tops[row]) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) {
+            const int u = y * kJoinThreads + threadIdx.x, row = 8 * (u / (N * 32)) + 2 * (u & 3);
+            if (u >= kUnits || row >= t.rows) continue;
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float4 v = reinterpret_cast<const float4*>(piece(i0 + i) + 16 * R)[u];
+                const float2 w = *reinterpret_cast<const float2*>(&weights[i][row]);
+                o[y].x += v.x * w.x;
+                o[y].y += v.y * w.y;
+                o[y].z += v.z * w.x;
+                o[y].w += v.w * w.y;
             }
         }
+    }
+#pragma unroll
+    for (int y = 0; y < kMine; ++y) {
+        const int u = y * kJoinThreads + threadIdx.x;
+        if (u >= kUnits) continue;
+        const int i = u / 32 % N, g = (u & 31) >> 2, row = 8 * (u / (N * 32)) + 2 * (u & 3);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int in_tile = row + e, r = t.first_row + in_tile;
             if (r >= p.m * p.G) continue;
-            const int q = r / p.G, h = hk * p.G + r % p.G;
-            const bool there = in_tile < t.rows && sums_l[in_tile] != 0.f;
-            const float inv = there ? 1.f / sums_l[in_tile] : 0.f;
-            const float a = there ? (e ? o.y : o.x) * inv : 0.f, b = there ? (e ? o.w : o.z) * inv : 0.f;
+            const int q = r / p.G, h = t.hk * p.G + r % p.G;
+            const bool there = in_tile < t.rows && sums[in_tile] != 0.f;
+            const float inv = there ? 1.f / sums[in_tile] : 0.f;
+            const float a = there ? (e ? o[y].y : o[y].x) * inv : 0.f, b = there ? (e ? o[y].w : o[y].z) * inv : 0.f;
             T* out = static_cast<T*>(p.out) + t.b * p.o_sb + h * p.o_sh + q * p.o_sn + Geo<D>::kVBytes * g + 2 * i;
             if constexpr (std::is_same<T, float>::value)
                 *reinterpret_cast<float2*>(out) = make_float2(a, b);
             else
                 *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(a, b);
             if (p.lse && g == 0 && i == 0)
-                p.lse[((int64_t)t.b * p.H + h) * p.m + q] = there ? (tops[in_tile] + log2f(sums_l[in_tile])) * kLn2 : -INFINITY;
+                p.lse[((int64_t)t.b * p.H + h) * p.m + q] = there ? (tops[in_tile] + log2f(sums[in_tile])) * kLn2 : -INFINITY;
         }
     }
 }
@@ -1001,7 +1019,7 @@ cudaError_t fwd_r(const CacheFwdParams& p, int num_sms, float* ws, cudaStream_t 
     k_fwd_cache<T, CODE, D, R><<<grid, kThreads, smem, counted(s)>>>(k_map, v_map, p, ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.B * row_tiles<R>(p) * p.c.Hk));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = counted(s);
     cudaLaunchAttribute attr;
@@ -1034,14 +1052,15 @@ cudaError_t fwd_code(const CacheFwdParams& p, int d, int num_sms, float* ws, cud
     }
 }
 
+template <typename T, int D, int R>
+constexpr int64_t block_floats() {
+    return blocks_per_sm<T, D, R>() * (2 * piece_floats<D, R>() + (int64_t)sizeof(Begun) / 4);
+}
 template <typename T, int D>
-constexpr int64_t workspace_per_sm() {  // two pieces a block
-    int64_t most = 0;
-    const int64_t r1 = 2 * blocks_per_sm<T, D, 1>() * piece_floats<D, 1>(), r2 = 2 * blocks_per_sm<T, D, 2>() * piece_floats<D, 2>(),
-                  r3 = 2 * blocks_per_sm<T, D, 3>() * piece_floats<D, 3>(), r4 = 2 * blocks_per_sm<T, D, 4>() * piece_floats<D, 4>();
-    most = r1 > r2 ? r1 : r2;
-    most = most > r3 ? most : r3;
-    return most > r4 ? most : r4;
+constexpr int64_t workspace_per_sm() {
+    const int64_t a = block_floats<T, D, 1>(), b = block_floats<T, D, 2>(), c = block_floats<T, D, 3>(), d = block_floats<T, D, 4>();
+    const int64_t ab = a > b ? a : b, cd = c > d ? c : d;
+    return ab > cd ? ab : cd;
 }
 
 }  // namespace
