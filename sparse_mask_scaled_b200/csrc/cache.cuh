@@ -94,4 +94,9 @@ int64_t fwd_cache_workspace(int real, int d, int num_sms);
 cudaError_t launch_fwd_cache(const CacheFwdParams& p, int real, int code, int d, int num_sms, float* ws,
                              cudaStream_t s);
 
+
+// Entry point of fwd_cache_tile.cu (bf16 queries).
+int64_t fwd_cache_tile_workspace(int d, int num_sms);
+cudaError_t launch_fwd_cache_tile(const CacheFwdParams& p, int code, int d, int num_sms, float* ws, cudaStream_t s);
+
 }  // namespace spattn

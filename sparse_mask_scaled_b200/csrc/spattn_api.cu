@@ -1450,6 +1450,9 @@ int check_cache(const spattn_cache* c, CacheView* v, int* code, int* d) {
     return SPATTN_OK;
 }
 
+// bf16 queries with more rows a K/V head than this take the tensor-core tiles.
+constexpr int kCacheTileRows = 32;
+
 // A [batch, heads, m, d] tensor beside a cache.
 int check_cache_rows(const spattn_tensor* t, const char* name, const CacheView& v, int64_t heads, int64_t m, int d,
                      int32_t dtype) {
@@ -2079,8 +2082,10 @@ int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const in
     CUDA_TRY(device_state(dev, &pool, &sms), "memory pool");
     const int real = q->dtype == SPATTN_BF16 ? 0 : 1;
     float* ws = nullptr;
-    CUDA_TRY(pool_alloc(&ws, fwd_cache_workspace(real, d, sms), pool, s), "cache attention workspace");
-    const cudaError_t e = launch_fwd_cache(p, real, code, d, sms, ws, s);
+    const bool tiles = real == 0 && (int64_t)p.m * p.G > kCacheTileRows;
+    CUDA_TRY(pool_alloc(&ws, tiles ? fwd_cache_tile_workspace(d, sms) : fwd_cache_workspace(real, d, sms), pool, s),
+             "cache attention workspace");
+    const cudaError_t e = tiles ? launch_fwd_cache_tile(p, code, d, sms, ws, s) : launch_fwd_cache(p, real, code, d, sms, ws, s);
     const cudaError_t ef = cudaFreeAsync(ws, s);
     if (e != cudaSuccess) return cuda_fail(e, "cache attention launch");
     if (ef != cudaSuccess) return cuda_fail(ef, "cudaFreeAsync");
