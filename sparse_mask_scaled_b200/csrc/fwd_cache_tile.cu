@@ -213,6 +213,13 @@ __device__ __forceinline__ void convert_role(const CacheFwdParams& p, TileShared
 }
 
 // ------------------------------------------------------------------ products
+// a * b + c, two fp32 lanes.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // Halves of a tile that have rows.
 __device__ __forceinline__ int halves(const Tile& t) { return t.rows > 128 ? 2 : 1; }
 
@@ -369,20 +376,16 @@ __device__ __forceinline__ void softmax_role(const CacheFwdParams& p, TileShared
                 const bool full = pages && (w.x < t.na ? j0 + kGroup <= full_a
                                                        : j0 + kGroup <= full_hi && (j0 >= full_lo || j0 + kGroup <= full_a));
                 const bool begin = w.x == part.first;
-                auto chunk = [&](const float (&s)[32], int c, auto all) {
-                    float x[32];
-                    auto exponents = [&](const float (&raw)[32], float ref) {
+                // 32 tokens: x holds their scores, then their exponents
+                auto chunk = [&](float (&x)[32], int c, auto all) {
+                    auto exponents = [&](float ref) {
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const float f = factor * sh.ks[slot][2 * c + b], a = sh.lv[slot][2 * c + b] - ref;
-                            const uint64_t f2 = pack2(f, f);
+                            const uint64_t f2 = pack2(f, f), a2 = pack2(a, a);
 #pragma unroll
-                            for (int y = 0; y < 16; y += 2) {
-                                x[16 * b + y] = a;
-                                x[16 * b + y + 1] = a;
-                                fma2_inplace(x[16 * b + y], x[16 * b + y + 1], __float_as_uint(raw[16 * b + y]),
-                                             __float_as_uint(raw[16 * b + y + 1]), f2);
-                            }
+                            for (int y = 16 * b; y < 16 * b + 16; y += 2)
+                                unpack2(fma2(pack2(x[y], x[y + 1]), f2, a2), x[y], x[y + 1]);
                         }
                         if constexpr (!decltype(all)::value) {
 #pragma unroll
@@ -403,9 +406,11 @@ __device__ __forceinline__ void softmax_role(const CacheFwdParams& p, TileShared
                         }
                         return fmax3(fmaxf(a, b), x[30], x[31]);
                     };
-                    exponents(s, m);
+                    exponents(m);
                     if (__any_sync(0xffffffffu, top() > kRescaleAt)) {
-                        exponents(s, 0.f);
+                        tmem_ld32f(s_at + 32 * c, x);  // the scores again: no weight lies over them yet
+                        tmem_wait_ld_depf(x);
+                        exponents(0.f);
                         const float raw = top(), ref = raw - m > kRescaleAt ? raw - kHeadroom : m, by = ex2(m - ref);
                         l *= by;
                         if (!begin) {  // the products into O issued so far are done: S came after them
@@ -452,17 +457,17 @@ __device__ __forceinline__ void softmax_role(const CacheFwdParams& p, TileShared
                     }
                     tmem_st16(s_at + 16 * c, h);
                 };
-                float s[2][32];
-                tmem_ld32f(s_at, s[0]);
-                tmem_wait_ld_depf(s[0]);
-#pragma unroll
+                // one chunk's registers at a time: a second one in flight spilled, and the other half's warps
+                // cover the load
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_ld32f(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+                    float x[32];
+                    tmem_ld32f(s_at + 32 * c, x);
+                    tmem_wait_ld_depf(x);
                     if (full)
-                        chunk(s[c & 1], c, std::true_type{});
+                        chunk(x, c, std::true_type{});
                     else
-                        chunk(s[c & 1], c, std::false_type{});
-                    if (c < 3) tmem_wait_ld_depf(s[(c + 1) & 1]);
+                        chunk(x, c, std::false_type{});
                 }
                 tmem_wait_st();
             }
