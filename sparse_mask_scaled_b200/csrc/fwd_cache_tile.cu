@@ -101,7 +101,7 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, volatil
 template <int CODE, int D, typename Part>
 __device__ __forceinline__ void convert_role(const CacheFwdParams& p, TileShared<D>& sh, Part part, int rts) {
     using G = TileGeo<D>;
-    const int tid = threadIdx.x - 256, lane = tid & 31;
+    const int tid = threadIdx.x & 127, lane = tid & 31;
     const int page_mask = (1 << p.c.page_shift) - 1;
     struct Step {
         int raw;  // the table's entry for sub-block lane % 8, kUnread where none is needed
@@ -128,63 +128,70 @@ __device__ __forceinline__ void convert_role(const CacheFwdParams& p, TileShared
         }
         return s;
     };
+    const int sub_lane = tid % G::kPerToken, first_token = tid / G::kPerToken;
+    constexpr int kTokens = 128 / G::kPerToken;  // of a pass, a multiple of 16
+    const int in_sub = first_token & 15;
+    // requests a step's codes of one side
+    auto load = [&](uint4 (&x)[G::kPasses], const CacheSide& side, const Step& s) {
+        int64_t at = -1;  // of this lane's sub-block
+        if (s.raw >= 0) at = s.raw * side.s_p + s.hk * side.s_h + ((s.j + 16 * (lane & 7)) & page_mask) * side.s_t;
+        const bool whole = s.j >= s.lo && s.j + kGroup <= s.hi;
+        const uint8_t* const mine = side.codes + in_sub * side.s_t + 16 * sub_lane;
+#pragma unroll
+        for (int i = 0; i < G::kPasses; ++i) {
+            const int o = i * kTokens + first_token;
+            const int64_t from = __shfl_sync(0xffffffffu, at, o >> 4);
+            x[i] = make_uint4(0, 0, 0, 0);  // tokens that no row may see: zeros, whatever their codes
+            if (from >= 0 && (whole || (s.j + o >= s.lo && s.j + o < s.hi)))
+                x[i] = __ldg(reinterpret_cast<const uint4*>(mine + from));
+        }
+    };
     auto check = [&](Step& s) {
         if ((unsigned)s.raw >= (unsigned)p.c.num_pages) {
             if (s.raw != kUnread) atomicOr(p.c.err, kErrBadPage);
             s.raw = -1;
         }
     };
-    const int sub_lane = tid % G::kPerToken, first_token = tid / G::kPerToken;
-    constexpr int kTokens = 128 / G::kPerToken;  // of a pass
-    auto load = [&](uint4 (&x)[G::kPasses], const CacheSide& side, const Step& s) {
-#pragma unroll
-        for (int i = 0; i < G::kPasses; ++i) {
-            const int o = i * kTokens + first_token, j = s.j + o;
-            const int pid = __shfl_sync(0xffffffffu, s.raw, o >> 4);
-            x[i] = make_uint4(0, 0, 0, 0);  // tokens that no row may see: zeros, whatever their codes
-            if (pid >= 0 && j >= s.lo && j < s.hi)
-                x[i] = __ldg(reinterpret_cast<const uint4*>(side.codes + pid * side.s_p + s.hk * side.s_h +
-                                                            (j & page_mask) * side.s_t + 16 * sub_lane));
-        }
-    };
     // sub-blocks whose bit in `zero` is set become zeros
     auto store = [&](const uint4 (&x)[G::kPasses], uint8_t* tile, unsigned zero) {
+        const bool swap = (sub_lane >> 2) & 1;  // half the lanes of a token the other way round: no bank conflicts
+        uint8_t* const first = tile + G::unit(first_token, 2 * sub_lane + swap);
+        uint8_t* const second = tile + G::unit(first_token, 2 * sub_lane + !swap);
 #pragma unroll
-        for (int i = 0; i < G::kPasses; ++i) {
-            const int o = i * kTokens + first_token;
+        for (int i = 0; i < G::kPasses; ++i) {  // rows a multiple of 16 apart are swizzled alike
             uint4 a, b;
             codes_to_half<CODE>(x[i].x, a.x, a.y);
             codes_to_half<CODE>(x[i].y, a.z, a.w);
             codes_to_half<CODE>(x[i].z, b.x, b.y);
             codes_to_half<CODE>(x[i].w, b.z, b.w);
-            if (zero >> (o >> 4) & 1) a = b = make_uint4(0, 0, 0, 0);
-            const bool swap = (sub_lane >> 2) & 1;  // half the lanes of a token the other way round: no bank conflicts
-            *reinterpret_cast<uint4*>(tile + G::unit(o, 2 * sub_lane + swap)) = swap ? b : a;
-            *reinterpret_cast<uint4*>(tile + G::unit(o, 2 * sub_lane + !swap)) = swap ? a : b;
-        }
-    };
-    auto scales = [&](const Step& s, float& ks, float& vs) {  // of sub-block lane % 8
-        ks = vs = kNoPage;
-        if (s.raw >= 0) {
-            const int64_t at = (int64_t)s.raw * p.c.Hk + s.hk;
-            ks = __ldg(p.c.k.scale + at);
-            vs = __ldg(p.c.v.scale + at);
+            if (zero >> ((i * kTokens + first_token) >> 4) & 1) a = b = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(first + i * kTokens * G::kRowBytes) = swap ? b : a;
+            *reinterpret_cast<uint4*>(second + i * kTokens * G::kRowBytes) = swap ? a : b;
         }
     };
     const uint32_t k_full = smem_u32(&sh.k_full[0]), k_empty = smem_u32(&sh.k_empty[0]), v_full = smem_u32(&sh.v_full[0]),
                    v_empty = smem_u32(&sh.v_empty[0]);
     Step now = look_up(), next = look_up();
-    check(now);
     uint4 kx[G::kPasses], vx[G::kPasses];
-    float ks, vs, ks_next = 0.f, vs_next = 0.f;
+    check(now);
     load(kx, p.c.k, now);
     load(vx, p.c.v, now);
-    scales(now, ks, vs);
+    float ks = kNoPage, vs = kNoPage;  // of sub-block lane % 8
+    auto scales = [&](const Step& s) {
+        ks = vs = kNoPage;
+        if (s.raw >= 0) {
+            const int64_t sc = (int64_t)s.raw * p.c.Hk + s.hk;
+            ks = __ldg(p.c.k.scale + sc);
+            vs = __ldg(p.c.v.scale + sc);
+        }
+    };
+    scales(now);
     for (uint32_t n = 0; now.more; ++n) {
         check(next);
         const Step after = look_up();
         if (!tile_wait(k_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, &sh.abort)) return;
         const bool none = vs < kMinScale;  // no page, or a scale that counts as 0: its values are zeros
+        const unsigned zero = __ballot_sync(0xffffffffu, none) & 0xffu;
         if (tid < 8) {
             const int slot = n % kParamSlots;
             sh.ks[slot][tid] = ks;
@@ -195,20 +202,18 @@ __device__ __forceinline__ void convert_role(const CacheFwdParams& p, TileShared
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + 8 * (n & 1));
-        if (next.more) load(kx, p.c.k, next);
+        if (next.more) {
+            load(kx, p.c.k, next);
+            scales(next);
+        }
         if (!tile_wait(v_empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, &sh.abort)) return;
-        store(vx, sh.v[n & 1], __ballot_sync(0xffffffffu, none) & 0xffu);
+        store(vx, sh.v[n & 1], zero);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + 8 * (n & 1));
-        if (next.more) {
-            load(vx, p.c.v, next);
-            scales(next, ks_next, vs_next);
-        }
+        if (next.more) load(vx, p.c.v, next);
         now = next;
         next = after;
-        ks = ks_next;
-        vs = vs_next;
     }
 }
 
@@ -566,15 +571,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_fwd_cache_tile(CacheFwdPara
         part.at = shares.start(blockIdx.x);
         part.end = shares.start(blockIdx.x + 1);
         line_find<kGroup, kRows, kTileThreads>(p, sh.sums, part.at, &part.entry, &part.place);
-        // registers: 256 x 176 + 128 x 112 + 128 x 48 = the launch's 512 x 128
+        // registers: 256 x 152 + 128 x 152 + 128 x 56 = the launch's 512 x 128
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
             softmax_role<D>(p, sh, part, rts, shares, ws);
         } else if (warp < 12) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
             convert_role<CODE, D>(p, sh, part, rts);
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
             if (warp == 12) product_role<D>(p, sh, part, rts);
         }
     }
