@@ -47,8 +47,11 @@ __device__ __forceinline__ Tile make_tile(const CacheFwdParams& p, int b, int rt
     const int64_t left = (int64_t)nq * p.G - t.first_row;
     t.rows = (int)(left < 0 ? 0 : left < ROWS ? left : ROWS);
     t.base = n - nq;
-    const int lo_pos = t.base + t.first_row / p.G;
-    const int hi_pos = t.base + (t.first_row + (t.rows > 0 ? t.rows : 1) - 1) / p.G;
+    int lo_pos = t.base, hi_pos = t.base + (nq > 0 ? nq : 1) - 1;  // of a sequence's only tile
+    if ((int64_t)p.m * p.G > ROWS) {
+        lo_pos = t.base + t.first_row / p.G;
+        hi_pos = t.base + (t.first_row + (t.rows > 0 ? t.rows : 1) - 1) / p.G;
+    }
     t.b_hi = t.rows > 0 && hi_pos >= 0 ? hi_pos + 1 : 0;
     const int win = p.window < 0 ? 0x7fffffff : p.window;
     t.b_lo = lo_pos > win ? lo_pos - win : 0;
@@ -70,59 +73,52 @@ __host__ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p) {
     return (int)(((int64_t)p.m * p.G + ROWS - 1) / ROWS);
 }
 
-// The line of all steps: entry e = (sequence, row tile) holds Hk segments one
-// after the other. Finds the total, and the entry that holds place `at` (in
-// steps of one head, times Hk) with its first place. Every thread of the block
-// calls it.
+// The line of all steps: entry e = (sequence, row tile) holds Hk segments one after
+// the other, each of the tile's groups. Every warp works it out for itself (no
+// barrier; a block's start counts in a token's step): lane x sums the entries
+// [x per, (x + 1) per).
+template <int GROUP, int ROWS>
 struct Line {
-    int64_t total;
-};
-template <int GROUP, int ROWS, int NT>
-__device__ Line line_total(const CacheFwdParams& p, int64_t (&sums)[NT + 1]) {
-    const int entries = p.B * row_tiles<ROWS>(p), per = (entries + NT - 1) / (NT);
-    const int tid = threadIdx.x;
-    int64_t mine = 0;
-    for (int e = tid * per; e < entries && e < (tid + 1) * per; ++e)
-        mine += make_tile<GROUP, ROWS>(p, e / row_tiles<ROWS>(p), e % row_tiles<ROWS>(p)).groups;
-    // inclusive scan over the block
-    int64_t x = mine;
+    int64_t total;   // places
+    int64_t before;  // places before this lane's entries
+    int per, entries, rts;
+    __device__ __forceinline__ int groups(const CacheFwdParams& p, int e) const {
+        return rts == 1 ? make_tile<GROUP, ROWS>(p, e, 0).groups : make_tile<GROUP, ROWS>(p, e / rts, e % rts).groups;
+    }
+    __device__ __forceinline__ explicit Line(const CacheFwdParams& p) {
+        rts = row_tiles<ROWS>(p);
+        entries = p.B * rts;
+        per = (entries + 31) >> 5;
+        const int lane = threadIdx.x & 31;
+        int64_t mine = 0;
+        for (int e = lane * per; e < entries && e < (lane + 1) * per; ++e) mine += groups(p, e);
+        mine *= p.c.Hk;
+        int64_t x = mine;
 #pragma unroll
-    for (int y = 1; y < 32; y <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, x, y);
-        if ((tid & 31) >= y) x += up;
+        for (int y = 1; y < 32; y <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, x, y);
+            if (lane >= y) x += up;
+        }
+        before = x - mine;
+        total = __shfl_sync(0xffffffffu, x, 31);
     }
-    sums[tid + 1] = x;
-    if (tid == 0) sums[0] = 0;
-    __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < (tid >> 5); ++w) before += sums[32 * (w + 1)];
-    __syncthreads();
-    sums[tid + 1] = x + before;
-    __syncthreads();
-    return Line{sums[NT] * p.c.Hk};
-}
-// The entry that holds place `at` < total, and its first place.
-template <int GROUP, int ROWS, int NT>
-__device__ void line_find(const CacheFwdParams& p, const int64_t (&sums)[NT + 1], int64_t at, int* entry,
-                          int64_t* first) {
-    const int per = (p.B * row_tiles<ROWS>(p) + NT - 1) / (NT);
-    int lo = 0, hi = NT - 1;  // the thread whose entries hold it
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid + 1] * p.c.Hk > at) hi = mid;
-        else lo = mid + 1;
+    // The entry that holds place `at` < total, and its first place.
+    __device__ __forceinline__ void find(const CacheFwdParams& p, int64_t at, int* entry, int64_t* first) const {
+        // the last lane whose entries begin at or before it (lanes behind the entries begin at `total`)
+        const int lane = 31 - __clz(__ballot_sync(0xffffffffu, before <= at));
+        int64_t place = __shfl_sync(0xffffffffu, before, lane);
+        int e = lane * per;
+        while (true) {
+            const int64_t len = (int64_t)groups(p, e) * p.c.Hk;
+            if (place + len > at) break;
+            place += len;
+            ++e;
+        }
+        *entry = e;
+        *first = place;
     }
-    int e = lo * per;
-    int64_t place = sums[lo] * p.c.Hk;
-    while (true) {
-        const int64_t len = (int64_t)make_tile<GROUP, ROWS>(p, e / row_tiles<ROWS>(p), e % row_tiles<ROWS>(p)).groups * p.c.Hk;
-        if (place + len > at) break;
-        place += len;
-        ++e;
-    }
-    *entry = e;
-    *first = place;
-}
+};
+
 // a / b for a >= 0, b > 0, in 32 bits where they fit (a fraction of the time).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
@@ -168,7 +164,7 @@ struct Part {
     int hk, first, last;  // of the current segment
     __device__ __forceinline__ bool open(const CacheFwdParams& p, int rts) {  // the segment that holds `at`
         if (at >= end) return false;
-        t = make_tile<GROUP, ROWS>(p, entry / rts, entry % rts);
+        t = rts == 1 ? make_tile<GROUP, ROWS>(p, entry, 0) : make_tile<GROUP, ROWS>(p, entry / rts, entry % rts);
         hk = (int)quotient(at - place, t.groups);
         first = (int)(at - place - (int64_t)hk * t.groups);
         last = end - at < t.groups - first ? first + (int)(end - at) : t.groups;  // one past

@@ -304,7 +304,6 @@ struct Shared {
     float scales[S][2][kWarps * Geo<D>::kSub];  // K, V of each sub-block
     uint64_t full[S], empty[S];
     JoinMl<R> ml;
-    int64_t sums[kThreads + 1];
 };
 constexpr int kRingAlign = 1024;  // the swizzle's period
 
@@ -471,14 +470,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
     Begun* const begun = reinterpret_cast<Begun*>(ws);
     float* const pieces = ws + (int64_t)gridDim.x * (sizeof(Begun) / 4);
     if (threadIdx.x == 0) begun[blockIdx.x].more = 0;
-    const Line line = line_total<Geo<D>::kGroup, 8 * R, kThreads>(p, sh.sums);  // (with barriers)
+    const Line<G::kGroup, 8 * R> line(p);
+    __syncthreads();  // the barriers are set up
     const Shares shares(line.total, (int)gridDim.x);
     if ((int)blockIdx.x >= shares.blocks) return;
-    const int rts = row_tiles<8 * R>(p);
+    const int rts = line.rts;
     Part<Geo<D>::kGroup, 8 * R> part;
     part.at = shares.start(blockIdx.x);
     part.end = shares.start(blockIdx.x + 1);
-    line_find<Geo<D>::kGroup, 8 * R, kThreads>(p, sh.sums, part.at, &part.entry, &part.place);
+    line.find(p, part.at, &part.entry, &part.place);
     if (warp == kWarps) {
         produce<D, R, kStages>(k_map, v_map, p, sh, part, rts);
         return;
@@ -706,79 +706,74 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
 // with: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its pieces.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) k_fwd_cache_join(CacheFwdParams p, const float* ws, int grid) {
-    constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32, kBatch = 32;
-    __shared__ float tops[8 * R], sums[8 * R], weights[kBatch][8 * R];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int N = Geo<D>::kSteps, kUnits = R * N * 32, kBatch = 16;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Begun t = reinterpret_cast<const Begun*>(ws)[blockIdx.x];
     if (t.more <= 0) return;
     const int np = t.more + 1;
     const float* const pieces = ws + (int64_t)grid * (sizeof(Begun) / 4);
-    auto piece = [&](int i) { return pieces + ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * piece_floats<D, R>(); };
-    // the rows' references and sums: a warp every fourth row, its lanes over the pieces
-    for (int row = warp; row < 8 * R; row += kJoinThreads / 32) {
-        float top = kNone, l = 0.f;
+    // a thread: 2 rows x 2 elements; 16 pieces' values and their rows' m and l on the way at a time
+    for (int u = threadIdx.x; u < kUnits; u += kJoinThreads) {
+        const int i = u / 32 % N, g = (u & 31) >> 2, row = 8 * (u / (N * 32)) + 2 * (u & 3);
+        if (t.first_row + row >= p.m * p.G) continue;
+        float top0 = kNone, top1 = kNone, l0 = 0.f, l1 = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < t.rows) {
-            for (int i = lane; i < np; i += 32) top = fmaxf(top, piece(i)[row]);
+            for (int x0 = 0; x0 < np; x0 += kBatch) {
+                float4 v[kBatch];
+                float2 m[kBatch], l[kBatch];
 #pragma unroll
-            for (int z = 1; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-            for (int i = lane; i < np; i += 32) l += ex2(piece(i)[row] - top) * piece(i)[8 * R + row];
+                for (int x = 0; x < kBatch; ++x) {
+                    m[x] = make_float2(kNone, kNone);
+                    l[x] = make_float2(0.f, 0.f);
+                    v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x0 + x < np) {
+                        const float* src = pieces + ((int64_t)(blockIdx.x + x0 + x) * 2 + (x0 + x == 0)) * piece_floats<D, R>();
+                        m[x] = *reinterpret_cast<const float2*>(src + row);
+                        l[x] = *reinterpret_cast<const float2*>(src + 8 * R + row);
+                        v[x] = reinterpret_cast<const float4*>(src + 16 * R)[u];
+                    }
+                }
+                float up0 = top0, up1 = top1;
 #pragma unroll
-            for (int z = 1; z < 32; z <<= 1) l += __shfl_xor_sync(0xffffffffu, l, z);
-        }
-        if (lane == 0) {
-            tops[row] = top;
-            sums[row] = l;
-        }
-    }
-    // a thread: 2 rows x 2 elements of kUnits / kJoinThreads places
-    constexpr int kMine = kUnits / kJoinThreads > 0 ? kUnits / kJoinThreads : 1;
-    float4 o[kMine];
+                for (int x = 0; x < kBatch; ++x) {
+                    up0 = fmaxf(up0, m[x].x);
+                    up1 = fmaxf(up1, m[x].y);
+                }
+                const float a0 = ex2(top0 - up0), a1 = ex2(top1 - up1);
+                top0 = up0;
+                top1 = up1;
+                l0 *= a0;
+                l1 *= a1;
+                o = make_float4(o.x * a0, o.y * a1, o.z * a0, o.w * a1);
 #pragma unroll
-    for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < np; i0 += kBatch) {
-        const int n = np - i0 < kBatch ? np - i0 : kBatch;
-        __syncthreads();
-        for (int x = threadIdx.x; x < n * 8 * R; x += kJoinThreads) {
-            const int row = x % (8 * R);
-            weights[x / (8 * R)][row] = row < t.rows ? ex2(piece(i0 + x / (8 * R))[row] - tops[row]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-            const int u = y * kJoinThreads + threadIdx.x, row = 8 * (u / (N * 32)) + 2 * (u & 3);
-            if (u >= kUnits || row >= t.rows) continue;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float4 v = reinterpret_cast<const float4*>(piece(i0 + i) + 16 * R)[u];
-                const float2 w = *reinterpret_cast<const float2*>(&weights[i][row]);
-                o[y].x += v.x * w.x;
-                o[y].y += v.y * w.y;
-                o[y].z += v.z * w.x;
-                o[y].w += v.w * w.y;
+                for (int x = 0; x < kBatch; ++x) {
+                    const float w0 = ex2(m[x].x - up0), w1 = ex2(m[x].y - up1);
+                    l0 = fmaf(w0, l[x].x, l0);
+                    l1 = fmaf(w1, l[x].y, l1);
+                    o.x = fmaf(w0, v[x].x, o.x);
+                    o.y = fmaf(w1, v[x].y, o.y);
+                    o.z = fmaf(w0, v[x].z, o.z);
+                    o.w = fmaf(w1, v[x].w, o.w);
+                }
             }
         }
-    }
-#pragma unroll
-    for (int y = 0; y < kMine; ++y) {
-        const int u = y * kJoinThreads + threadIdx.x;
-        if (u >= kUnits) continue;
-        const int i = u / 32 % N, g = (u & 31) >> 2, row = 8 * (u / (N * 32)) + 2 * (u & 3);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int in_tile = row + e, r = t.first_row + in_tile;
             if (r >= p.m * p.G) continue;
             const int q = r / p.G, h = t.hk * p.G + r % p.G;
-            const bool there = in_tile < t.rows && sums[in_tile] != 0.f;
-            const float inv = there ? 1.f / sums[in_tile] : 0.f;
-            const float a = there ? (e ? o[y].y : o[y].x) * inv : 0.f, b = there ? (e ? o[y].w : o[y].z) * inv : 0.f;
+            const float l = e ? l1 : l0;
+            const bool there = in_tile < t.rows && l != 0.f;
+            const float inv = there ? 1.f / l : 0.f;
+            const float a = there ? (e ? o.y : o.x) * inv : 0.f, b = there ? (e ? o.w : o.z) * inv : 0.f;
             T* out = static_cast<T*>(p.out) + t.b * p.o_sb + h * p.o_sh + q * p.o_sn + Geo<D>::kVBytes * g + 2 * i;
             if constexpr (std::is_same<T, float>::value)
                 *reinterpret_cast<float2*>(out) = make_float2(a, b);
             else
                 *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(a, b);
             if (p.lse && g == 0 && i == 0)
-                p.lse[((int64_t)t.b * p.H + h) * p.m + q] = there ? (tops[in_tile] + log2f(sums[in_tile])) * kLn2 : -INFINITY;
+                p.lse[((int64_t)t.b * p.H + h) * p.m + q] = there ? ((e ? top1 : top0) + log2f(l)) * kLn2 : -INFINITY;
         }
     }
 }

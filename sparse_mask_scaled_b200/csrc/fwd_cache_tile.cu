@@ -76,7 +76,6 @@ struct TileShared {
     uint64_t drain;
     uint32_t tmem;
     volatile int abort;
-    int64_t sums[kTileThreads + 1];
 };
 
 template <int D>
@@ -562,15 +561,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_fwd_cache_tile(CacheFwdPara
     }
     if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
     tc_fence_before();
-    const Line line = line_total<kGroup, kRows, kTileThreads>(p, sh.sums);  // (with barriers)
+    const Line<kGroup, kRows> line(p);
+    __syncthreads();  // the barriers and the tensor memory's address are there
     tc_fence_after();
     const Shares shares(line.total, (int)gridDim.x);
     if ((int)blockIdx.x < shares.blocks) {
-        const int rts = row_tiles<kRows>(p);
+        const int rts = line.rts;
         Part<kGroup, kRows> part;
         part.at = shares.start(blockIdx.x);
         part.end = shares.start(blockIdx.x + 1);
-        line_find<kGroup, kRows, kTileThreads>(p, sh.sums, part.at, &part.entry, &part.place);
+        line.find(p, part.at, &part.entry, &part.place);
         // registers: 256 x 152 + 128 x 152 + 128 x 56 = the launch's 512 x 128
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
