@@ -75,6 +75,12 @@ __device__ __forceinline__ uint32_t exact_code(float x, float s) {
     return (uint32_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
+// Four of them; kept out of line, since it is rare and long.
+template <int CODE>
+__device__ __noinline__ uint32_t exact_codes(float a, float b, float c, float d, float s) {
+    return exact_code<CODE>(a, s) | exact_code<CODE>(b, s) << 8 | exact_code<CODE>(c, s) << 16 | exact_code<CODE>(d, s) << 24;
+}
+
 // The codes of finite x[0..V), |x| <= qmax s (1 + 2^-23), and inv = 1 / s rounded.
 // x inv is off from the fp32 quotient by less than 4 units in the last place, so
 // the two round to the same code unless a border lies that near: for int8 a half,
@@ -118,9 +124,7 @@ __device__ __forceinline__ void make_codes(const float (&x)[V], float s, float i
     }
     if (divide) {
 #pragma unroll
-        for (int y = 0; y < V / 4; ++y) w[y] = 0;
-#pragma unroll
-        for (int y = 0; y < V; ++y) w[y / 4] |= exact_code<CODE>(x[y], s) << (8 * (y % 4));
+        for (int y = 0; y < V / 4; ++y) w[y] = exact_codes<CODE>(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3], s);
     }
 }
 
