@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 const float vs = vsc[sb];
                 const bool none = !full && vs < kMinScale;
                 ks[sb] = ksc[sb];
-                lv[sb] = none ? 0.f : sm100::lg2(vs);
+                lv[sb] = none ? 0.f : kParts == 2 ? log2f(vs) : sm100::lg2(vs);
                 inv_vs[sb] = none ? 1.f : __frcp_rn(vs);
             }
             auto exponents = [&](bool from_zero) {
