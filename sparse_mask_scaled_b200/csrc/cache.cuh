@@ -19,6 +19,11 @@ constexpr int kCodeI8 = 0;
 constexpr int kCodeE4m3 = 1;
 constexpr int kMinPage = 16, kMaxPage = 256;
 
+// Device error flag bits of the cache calls, beside those of spattn_internal.cuh. (That
+// header is part of what the other kernels' profiles are hashed over: it stays as it is.)
+constexpr unsigned kErrBadPage = 4u;    // a cache place without a page of the pool was left out
+constexpr unsigned kErrNonFinite = 8u;  // a NaN or an infinity was written to a cache
+
 struct CacheSide {  // K or V
     uint8_t* codes;
     float* scale;           // [num_pages, Hk]

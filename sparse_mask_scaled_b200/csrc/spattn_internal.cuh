@@ -13,8 +13,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // device error flag bits (read by spattn_device_error)
 constexpr unsigned kErrBadColumn = 1u;
 constexpr unsigned kErrTimeout = 2u;  // a bounded wait of the tensor-core kernel expired
-constexpr unsigned kErrBadPage = 4u;    // a cache place without a page of the pool was left out
-constexpr unsigned kErrNonFinite = 8u;  // a NaN or an infinity was written to a cache
 
 // Tensor-core tiling: 128 query rows by 128 keys.
 constexpr int kTileM = 128;

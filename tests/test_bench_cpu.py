@@ -52,3 +52,11 @@ def test_committed_summaries_parse():
         assert "- dram_bytes_per_launch: " in text, name
         seen += 1
     assert seen >= 1
+
+
+def test_committed_summaries_are_of_the_current_sources():
+    # the bench takes its DRAM traffic from them, and gives none for a kernel whose sources changed since
+    for kernel, workload in (("k_fwd_pp<64,1,1>", "block-strided-global"), ("k_fwd_pp<128,0,0>", "dense-d128"),
+                             ("k_fwd_short<64>", "random-csr"), ("k_fwd_tc_quad<64,0,0>", "variable-window"),
+                             ("k_fwd_tc_quad<32,1,1>", "evoformer-dense-mask-bias")):
+        assert bench.committed_traffic(kernel, workload) is not None, (kernel, workload)
