@@ -442,9 +442,13 @@ int spattn_cache_read(const spattn_cache* cache, const int32_t* start, const int
  * Rows without a token (t >= qlen[b], or pos < 0) give out = 0 and lse = -inf.
  * Tokens at and behind seqlen[b] are never used, whatever their codes; a token
  * whose codes are NaN (E4M3 only; spattn_cache_write writes none) must not be
- * attended to by any query of the call. Takes a workspace (at most about 40 MB)
- * from the library's stream-ordered pool for the call. A bounded wait that
- * expires raises device error flag bit 1. Stream-ordered, never synchronises.
+ * attended to by any query of the call. A V scale below 2^-100 counts as 0. A page
+ * with a V scale of 0 adds nothing to out and its share to the sum of weights; the
+ * sum loses weights where V scales above 2^30 stand beside such pages, or where V
+ * scales that are not 0 lie more than a factor of 2^74 apart.
+ * Takes a workspace (at most about 40 MB) from the library's stream-ordered pool for
+ * the call. A bounded wait that expires raises device error flag bit 1.
+ * Stream-ordered, never synchronises.
  * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
 int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const int32_t* seqlen,
                      const int32_t* qlen, int32_t window, int32_t n_global, float scale,

@@ -13,6 +13,11 @@ constexpr float kNone = -1e30f;      // reference of a row without a token so fa
 constexpr float kRescaleAt = 12.f;   // largest exponent of a weight before the reference moves
 constexpr float kHeadroom = 5.f;     // exponent of the largest weight after it moved
 constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100: a V scale below it counts as 0
+// In place of the log2 of such a scale, and of 1 / scale. Its tokens count in l alone. A small
+// substitute, so that they do not raise the reference above what the pages with values need (taken as
+// 1, they left weights of V scales of 2^-24 no bits in fp16); not so small that their weights leave
+// the range of fp32 beside V scales up to 2^30.
+constexpr float kNoValues = -64.f, kNoValuesInv = 1.8446744073709552e19f;  // 2^64
 
 constexpr long long kCacheWaitCycles = 2000000000LL;  // limit of a wait for a copy: about one second
 constexpr int kUnread = -0x7fffffff; // page of a sub-block that needs none

@@ -18,7 +18,8 @@
 //
 // Scales. A page's K scale multiplies its scores. Its V scale vs goes into the
 // exponent: p' = 2^(x + log2 vs - m) with x the score in base 2, so that weights
-// are largest where p v is, whatever the scales; O = sum p' c, l = sum p' / vs.
+// are largest where p v is, whatever the scales; O = sum p' c, l = sum p' / vs. A page
+// whose scale is 0 is taken to have a small one and no values.
 // Weights are rounded to fp16 for P V (11 bits; bf16 outputs have 8). m is a
 // reference that moves only when some p' would pass 2^12 (it then becomes the
 // largest exponent - 5), so that most steps need no exchange between lanes.
@@ -538,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 const float vs = vsc[sb];
                 const bool none = !full && vs < kMinScale;
                 ks[sb] = ksc[sb];
-                lv[sb] = none ? 0.f : kParts == 2 ? log2f(vs) : sm100::lg2(vs);
-                inv_vs[sb] = none ? 1.f : __frcp_rn(vs);
+                lv[sb] = none ? kNoValues : kParts == 2 ? log2f(vs) : sm100::lg2(vs);
+                inv_vs[sb] = none ? kNoValuesInv : __frcp_rn(vs);
             }
             auto exponents = [&](bool from_zero) {
 #pragma unroll

@@ -194,8 +194,8 @@ __device__ __forceinline__ void convert_role(const CacheFwdParams& p, TileShared
         if (tid < 8) {
             const int slot = n % kParamSlots;
             sh.ks[slot][tid] = ks;
-            sh.lv[slot][tid] = none ? 0.f : lg2(vs);
-            sh.inv[slot][tid] = none ? 1.f : __frcp_rn(vs);
+            sh.lv[slot][tid] = none ? kNoValues : lg2(vs);
+            sh.inv[slot][tid] = none ? kNoValuesInv : __frcp_rn(vs);
         }
         store(kx, sh.k[n & 1], 0u);
         fence_proxy_async_smem();

@@ -1,0 +1,115 @@
+"""Attention over the 8-bit cache where weights and V scales are small beside others: pages of zeros,
+scales of many sizes, pages that are missing, on every kernel."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import cache_exact
+import cache_reference as ref
+from cache_reference import CODES
+
+if torch.cuda.is_available():
+    import sparse_mask_scaled_b200 as sp
+
+REAL = {"bf16": torch.bfloat16, "f32": torch.float32}
+# (H, Hk, m): one row, 24 rows and 130 rows a K/V head
+ROWS = [(2, 2, 1), (8, 1, 3), (2, 2, 130)]
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    sp.spattn_device_error()
+    yield
+    assert sp.spattn_device_error() == 0
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def dev_cache(codes, scales, table, dtype):
+    return sp.Cache(codes[0].cuda().view(dtype), codes[1].cuda().view(dtype), scales[0].cuda(), scales[1].cuda(),
+                    table.cuda())
+
+
+def check(q, codes, scales, table, seqlen, dtype, used=None, gone=(), **kw):
+    """used: the table that the call gets (`table`: the one without missing pages)."""
+    cache = dev_cache(codes, scales, table if used is None else used, dtype)
+    out, lse = sp.spattn_fwd_cache(q.cuda(), cache, ints(seqlen).cuda(), **kw)
+    flags = sp.spattn_device_error()
+    want, want_lse, tol, tol_lse = cache_exact.attend(q, codes, scales, table, seqlen, [q.shape[2]] * len(seqlen), dtype,
+                                                      gone=gone, **kw)
+    out, lse = out.double().cpu(), lse.double().cpu().view(want_lse.shape)
+    some = ~torch.isneginf(want_lse)
+    assert torch.equal(torch.isneginf(lse), ~some) and bool((out[~some] == 0).all())
+    off = (out - want).abs()
+    assert bool((off <= tol).all()), float((off / tol.clamp(min=1e-300)).max())
+    gap = (lse - want_lse).abs()[some]
+    assert bool((gap <= tol_lse[some]).all()), float((gap / tol_lse[some]).max())
+    return flags
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("size", [-14, -24, -30, 12])
+def test_a_page_of_zeros_among_the_values(size, rows, code, real):
+    """The zero page's tokens count in the sum of weights and leave the other pages' weights their bits,
+    whether it comes first, in the middle or last."""
+    (H, Hk, m), dtype, g = rows, CODES[code], torch.Generator().manual_seed(40 + size)
+    n = [300, 290, 200]
+    codes, scales, table = ref.make_cache(g, 3, Hk, 16, 64, n, dtype)
+    scales[1].copy_(torch.where(torch.isnan(scales[1]), scales[1], 2.0 ** size * (1 + torch.rand(scales[1].shape, generator=g))))
+    for b, slot in enumerate((0, 7, 12)):
+        scales[1][table[b, slot]] = 0.0
+    q = torch.randn((3, H, m, 64), generator=g).to(REAL[real])
+    assert check(q, codes, scales, table, n, dtype) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_values_that_are_all_zero(rows, real):
+    (H, Hk, m), dtype, g = rows, torch.int8, torch.Generator().manual_seed(6)
+    codes, scales, table = ref.make_cache(g, 1, Hk, 32, 32, [333], dtype)
+    scales[1].fill_(0.0)
+    assert check(torch.randn((1, H, m, 32), generator=g).to(REAL[real]), codes, scales, table, [333], dtype) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_value_scales_of_many_sizes(rows, code, real):
+    (H, Hk, m), dtype, g = rows, CODES[code], torch.Generator().manual_seed(41)
+    codes, scales, table = ref.make_cache(g, 2, Hk, 16, 128, [260, 190], dtype)
+    s = scales[1]
+    s.copy_(torch.where(torch.isnan(s), s, 2.0 ** torch.randint(-30, 11, s.shape, generator=g).float()))
+    s[table[0, 3]] = 0.0
+    s[table[1, 11], 0] = 0.0
+    assert check(torch.randn((2, H, m, 128), generator=g).to(REAL[real]), codes, scales, table, [260, 190], dtype) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_pages_that_are_missing(rows, real):
+    (H, Hk, m), dtype, g = rows, torch.float8_e4m3fn, torch.Generator().manual_seed(43)
+    codes, scales, table = ref.make_cache(g, 2, Hk, 16, 64, [330, 200], dtype)
+    used = table.clone()
+    used[0, 5], used[0, 20], used[1, 0] = 1 << 20, -7, -1
+    q = torch.randn((2, H, m, 64), generator=g).to(REAL[real])
+    assert check(q, codes, scales, table, [330, 200], dtype, used=used, gone={(0, 5), (0, 20), (1, 0)}) == 4
+
+
+def test_the_status_of_each_cache_fault():
+    table = ints([[0, 1]]).cuda()
+    cache = sp.Cache.empty(2, 1, 16, 32, table, dtype=torch.int8)
+    x = torch.ones((1, 1, 3, 32), device="cuda")
+    sp.spattn_cache_write(x, x, cache, ints([30]).cuda())                 # behind the table
+    assert sp.spattn_check_device_error() == sp.SPATTN_ERR_BAD_CACHE
+    assert sp.spattn_check_device_error() == sp.SPATTN_OK
+    x[0, 0, 1, 3] = math.inf
+    sp.spattn_cache_write(x, x, cache)
+    assert sp.spattn_check_device_error() == sp.SPATTN_ERR_BAD_CACHE
+    assert sp.spattn_device_error() == 0
