@@ -14,15 +14,17 @@
 // once a row is scaled by a power of two that brings its largest element to
 // [2^14, 2^15) (elements 2^-28 below it lose bits): K Q^T is exact up to fp32
 // accumulation. fp32 queries and their weights go in as the sum of two fp16
-// numbers (22 bits), at twice the products.
+// numbers (22 bits), at twice the products; a weight's second number is held 2^11
+// times as large and meets V codes 2^-11 times as large, so that light weights,
+// whose first number has few bits left or none, keep theirs.
 //
 // Scales. A page's K scale multiplies its scores. Its V scale vs goes into the
 // exponent: p' = 2^(x + log2 vs - m) with x the score in base 2, so that weights
 // are largest where p v is, whatever the scales; O = sum p' c, l = sum p' / vs. A page
 // whose scale is 0 is taken to have a small one and no values.
 // Weights are rounded to fp16 for P V (11 bits; bf16 outputs have 8). m is a
-// reference that moves only when some p' would pass 2^12 (it then becomes the
-// largest exponent - 5), so that most steps need no exchange between lanes.
+// reference that moves only when some p' would pass 2^15 (it then becomes the
+// largest exponent - 8), so that most steps need no exchange between lanes.
 //
 // Streaming. The kernel is bound by HBM at long caches: each code is read once.
 // A producer warp fills a ring in shared memory by TMA: a copy brings 16 tokens
@@ -103,10 +105,17 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// What the fp16 pair `h` leaves of (a, b), as another one.
-__device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t h) {
+// What the fp16 pair `h` leaves of (a, b), times `by`, as another one.
+__device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t h, float by) {
     const __half2 v = *reinterpret_cast<const __half2*>(&h);
-    return half_pair(a - __low2float(v), b - __high2float(v));
+    return half_pair((a - __low2float(v)) * by, (b - __high2float(v)) * by);
+}
+constexpr float kRestScale = 2048.f;  // 2^11, of a weight's second part
+// An fp16 pair of codes times 2^-11: exact (multiples of 2^-20).
+__device__ __forceinline__ uint32_t rest_codes(uint32_t x) {
+    uint32_t y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x10001000u));
+    return y;
 }
 
 // Transposes an 8 x 8 matrix of fp16 held as lane (g, c): row g, columns 2 c, 2 c + 1.
@@ -360,7 +369,7 @@ __device__ __forceinline__ void load_query(const CacheFwdParams& p, const Tile& 
             for (int y = 0; y < 2; ++y) {
                 const float v0 = x[4 * s + 2 * y] * by, v1 = x[4 * s + 2 * y + 1] * by;
                 q.b[0][k][s][y] = half_pair(v0, v1);
-                if constexpr (parts<T>() == 2) q.b[1][k][s][y] = half_rest(v0, v1, q.b[0][k][s][y]);
+                if constexpr (parts<T>() == 2) q.b[1][k][s][y] = half_rest(v0, v1, q.b[0][k][s][y], 1.f);
             }
     }
 }
@@ -625,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                         const float p0 = e[k][sb][2 * x], p1 = e[k][sb][2 * x + 1];
                         const uint32_t h = half_pair(p0, p1);
                         pb[0][k][x] = transpose8(h);
-                        if constexpr (kParts == 2) pb[1][k][x] = transpose8(half_rest(p0, p1, h));
+                        if constexpr (kParts == 2) pb[1][k][x] = transpose8(half_rest(p0, p1, h, kRestScale));
                     }
                 uint32_t v[4][(G::kVBytes + 3) / 4];
 #pragma unroll
@@ -648,9 +657,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                         codes_to_half<CODE>(__byte_perm(v[0][y], v[1][y], pick), a[0], a[1]);
                         codes_to_half<CODE>(__byte_perm(v[2][y], v[3][y], pick), a[2], a[3]);
 #pragma unroll
-                        for (int k = 0; k < R; ++k)
+                        for (int k = 0; k < R; ++k) mma_f16(st.o[k][2 * y + z], a, pb[0][k][0], pb[0][k][1]);
+                        if constexpr (kParts == 2) {
 #pragma unroll
-                            for (int w = 0; w < kParts; ++w) mma_f16(st.o[k][2 * y + z], a, pb[w][k][0], pb[w][k][1]);
+                            for (int x = 0; x < 4; ++x) a[x] = rest_codes(a[x]);
+#pragma unroll
+                            for (int k = 0; k < R; ++k) mma_f16(st.o[k][2 * y + z], a, pb[1][k][0], pb[1][k][1]);
+                        }
                     }
             }
         };

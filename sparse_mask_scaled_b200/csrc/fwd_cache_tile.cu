@@ -15,7 +15,7 @@
 //
 // Numbers are held as in fwd_cache.cu: codes and scaled queries exact in fp16, fp32
 // accumulators, exponents p' = 2^(x + log2 vs - m) with a reference m that moves
-// only when a weight would pass 2^12; then O, l and the group's P so far are scaled.
+// only when a weight would pass 2^15; then O, l and the group's P so far are scaled.
 //
 // What bounds it: a 128 x 128 step of d = 128 is two 512-cycle products, 1024
 // cycles of exponentials (16 a cycle) and about as many of the softmax's other

@@ -21,9 +21,10 @@ def attend(q, codes, scales, table, seqlen, qlen, dtype, window=-1, n_global=0, 
     each. All that counts in the numerator and in the denominator, relative to sum_j p_j |v_j|.
 
     Weights are held in fp16 (bf16 queries), rounded once, and again where the reference moves: 2 * 2^-11; in two
-    such parts (fp32): 2^-22. The largest p_j * vs_j of a row (vs_j its V scale, at least 2^-64 here) is held as 2^5
-    or more, and fp16 is rounded by at most 2^-25 however small the weight is: a token is off by 2^-30 (twice for
-    bf16) times that and the largest code. The result is rounded at the end."""
+    such parts, the second 2^11 times as large (fp32): 2^-22. The largest p_j * vs_j of a row (vs_j its V scale, at
+    least 2^-64 here) is held as 2^8 or more, and fp16 is rounded by at most 2^-25 however small the weight is: a
+    token is off by 2^-33 (twice for bf16, 2^-44 for fp32) times that and the largest code. The result is rounded
+    at the end."""
     B, H, m, d = q.shape
     group = H // codes[0].shape[1]
     page, qmax = codes[0].shape[2], ref.QMAX[dtype]
@@ -60,7 +61,7 @@ def attend(q, codes, scales, table, seqlen, qlen, dtype, window=-1, n_global=0, 
         L = torch.where(vs > 0, vs, torch.ones_like(vs)).log2().abs().amax(1)[:, None]
         A = 1.45 * S + L + 15
         off = (d + 4) * 2.0 ** -23 * S + 2.0 ** -22 * (1.1 * A + 0.7 * L) + 2.0 ** -21 + (n / 16 + 32) * 2.0 ** -23
-        round_p, round_o, least = (2.0 ** -10, 2.0 ** -8, 2.0 ** -29) if half else (2.0 ** -22, 2.0 ** -24, 2.0 ** -30)
+        round_p, round_o, least = (2.0 ** -10, 2.0 ** -8, 2.0 ** -32) if half else (2.0 ** -22, 2.0 ** -24, 2.0 ** -44)
         of_token = scales[1][table[b, :-(-n // page)].long()].double().t().repeat_interleave(group, 0)
         of_token = of_token.repeat_interleave(page, 1)[:, None, :n].clamp(min=2.0 ** -64)
         floor = n * least * qmax * (p * of_token).amax(-1)

@@ -1,5 +1,5 @@
 """Attention over the 8-bit cache where weights and V scales are small beside others: pages of zeros,
-scales of many sizes, pages that are missing, on every kernel."""
+one token that outweighs all others, scales of many sizes, pages that are missing, on every kernel."""
 import math
 
 import pytest
@@ -89,6 +89,47 @@ def test_value_scales_of_many_sizes(rows, code, real):
     s[table[0, 3]] = 0.0
     s[table[1, 11], 0] = 0.0
     assert check(torch.randn((2, H, m, 128), generator=g).to(REAL[real]), codes, scales, table, [260, 190], dtype) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("at", [0, 4000])
+def test_one_token_that_outweighs_all_others(at, rows, real):
+    """Its value is zero, so that the result is what the small weights (2^-30.4 of its own) add up to."""
+    (H, Hk, m), n, d, dtype = rows, 4200, 32, torch.int8
+    table = torch.randperm(17, generator=torch.Generator().manual_seed(2)).int()[None, :]
+    codes = [torch.zeros((17, Hk, 256, d), dtype=torch.int8) for _ in range(2)]
+    codes[1].fill_(100)
+    codes[0][table[0, at // 256], :, at % 256, 0] = 127
+    codes[1][table[0, at // 256], :, at % 256] = 0
+    scales = [torch.full((17, Hk), 1.0 / 127), torch.full((17, Hk), 2.0 ** -7)]
+    q = torch.zeros((1, H, m, d), dtype=REAL[real])
+    q[..., 0] = 1.0
+    assert check(q, codes, scales, table, [n], dtype, scale=30.4 * math.log(2.0)) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
+def test_tokens_that_outweigh_the_others_of_whole_sequences(rows, real):
+    """As above with 448 heavy tokens, of a batch so large that a sequence is not shared out over the GPU:
+    the light tokens meet the heavy ones' reference everywhere. The sequences share their pages."""
+    (H, Hk, m), n, d, B, dtype = rows, 1500, 32, 320, torch.int8
+    table = ints([[3, 0, 4, 1, 5, 2]])
+    codes = [torch.zeros((6, Hk, 256, d), dtype=torch.int8) for _ in range(2)]
+    codes[1].fill_(100)
+    for j in range(448):
+        codes[0][table[0, j // 256], :, j % 256, 0] = 127
+        codes[1][table[0, j // 256], :, j % 256] = 0
+    scales = [torch.full((6, Hk), 1.0 / 127), torch.full((6, Hk), 2.0 ** -7)]
+    q = torch.zeros((1, H, m, d), dtype=REAL[real])
+    q[..., 0] = 1.0
+    kw = dict(scale=30.4 * math.log(2.0))
+    want, want_lse, tol, tol_lse = cache_exact.attend(q, codes, scales, table, [n], [m], dtype, **kw)
+    cache = dev_cache(codes, scales, table.expand(B, -1).contiguous(), dtype)
+    out, lse = sp.spattn_fwd_cache(q.expand(B, -1, -1, -1).cuda(), cache, ints([n] * B).cuda(), **kw)
+    off = (out.double().cpu() - want).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    assert bool(((lse.double().cpu().view(B, H, m) - want_lse).abs() <= tol_lse).all())
 
 
 @pytest.mark.parametrize("real", ["bf16", "f32"])
