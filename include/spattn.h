@@ -442,7 +442,10 @@ int spattn_cache_read(const spattn_cache* cache, const int32_t* start, const int
  * Rows without a token (t >= qlen[b], or pos < 0) give out = 0 and lse = -inf.
  * Tokens at and behind seqlen[b] are never used, whatever their codes; a token
  * whose codes are NaN (E4M3 only; spattn_cache_write writes none) must not be
- * attended to by any query of the call. A V scale below 2^-100 counts as 0. A page
+ * attended to by any query of the call. Sums, maxima and the accumulators of both
+ * products are fp32. With bf16 queries the softmax weights are rounded to 11 bits for
+ * the product with V; with f32 queries both products keep 22 bits or more of each
+ * factor. A V scale below 2^-100 counts as 0. A page
  * with a V scale of 0 adds nothing to out and its share to the sum of weights; the
  * sum loses weights where V scales above 2^30 stand beside such pages, or where V
  * scales that are not 0 lie more than a factor of 2^74 apart.

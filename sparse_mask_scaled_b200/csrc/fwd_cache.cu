@@ -13,10 +13,7 @@
 // one K/V head is a segment. Codes are exact in fp16, and so are bf16 queries
 // once a row is scaled by a power of two that brings its largest element to
 // [2^14, 2^15) (elements 2^-28 below it lose bits): K Q^T is exact up to fp32
-// accumulation. fp32 queries and their weights go in as the sum of two fp16
-// numbers (22 bits), at twice the products; a weight's second number is held 2^11
-// times as large and meets V codes 2^-11 times as large, so that light weights,
-// whose first number has few bits left or none, keep theirs.
+// accumulation.
 //
 // Scales. A page's K scale multiplies its scores. Its V scale vs goes into the
 // exponent: p' = 2^(x + log2 vs - m) with x the score in base 2, so that weights
@@ -25,6 +22,15 @@
 // Weights are rounded to fp16 for P V (11 bits; bf16 outputs have 8). m is a
 // reference that moves only when some p' would pass 2^15 (it then becomes the
 // largest exponent - 8), so that most steps need no exchange between lanes.
+//
+// fp32. Queries and weights go in as the sum of two fp16 numbers (24 bits with their
+// signs), at twice the products. A weight's second number is held 2^11 times as large
+// and meets V codes 2^-11 times as large, so that light weights, whose first number has
+// few bits left or none, keep theirs. The tensor cores' accumulation truncates, so the
+// second parts' scores have sums of their own, and each 16 tokens' P V starts at 0 and
+// is added to O by ordinary sums. m is a whole number, and of vs only the power of two
+// goes into the exponent; the rest is a factor of the weight. The error against 64 bits
+// is 0.2 to 0.3e-6 of out where torch operations in fp32 have 0.2 to 0.9e-6.
 //
 // Streaming. The kernel is bound by HBM at long caches: each code is read once.
 // A producer warp fills a ring in shared memory by TMA: a copy brings 16 tokens
@@ -124,6 +130,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+
+// fp32: two fp16 parts.
+template <typename T>
+constexpr int parts() {
+    return std::is_same<T, float>::value ? 2 : 1;
+}
+// How far a weight's exponent may pass 0 before the reference moves, and what the weights are multiplied by
+// on their way into P V (O is that much too large; m and l are not). fp32: the reference is the whole number
+// below the largest exponent, since an exponent near 0 is rounded least, and the weights are lifted after the
+// exponential; with the rest of vs they stay below 2^4 * 2 * 2^10.
+template <typename T>
+constexpr float kMoveAt = parts<T>() == 2 ? 4.f : kRescaleAt;
+template <typename T>
+constexpr float kLift = parts<T>() == 2 ? 1024.f : 1.f;
 
 // A tile's running state in one warp: lane (g = lane / 4, c = lane % 4) holds rows
 // 8 k + 2 c + e. o[k][i][2 x + e] is element kVBytes g + 2 i + x of that row; l is
@@ -246,7 +266,7 @@ __device__ __forceinline__ void write_rows(const CacheFwdParams& p, const Tile& 
             if (row >= p.m * p.G) continue;
             const int b = tile.b, t = row / p.G, h = hk * p.G + row % p.G;
             const bool there = in_tile < tile.rows && s.l[k][e] != 0.f;
-            const float inv = 1.f / s.l[k][e];
+            const float inv = 1.f / (kLift<T> * s.l[k][e]);
             T* out = static_cast<T*>(p.out) + b * p.o_sb + h * p.o_sh + t * p.o_sn + N * g;
             float v[N];
 #pragma unroll
@@ -289,11 +309,6 @@ __device__ __forceinline__ void write_piece(float* ws, const State<D, R>& s, int
 #pragma unroll
         for (int i = 0; i < N; ++i) reinterpret_cast<float4*>(ws + 16 * R)[(k * N + i) * 32 + lane] = s.get(k, i);
     }
-}
-// fp32: two fp16 parts.
-template <typename T>
-constexpr int parts() {
-    return std::is_same<T, float>::value ? 2 : 1;
 }
 // Blocks an SM holds: with 128 registers a thread two, else one. O, Q and the
 // scores take `held` of them.
@@ -518,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 for (int sb = 0; sb < G::kSub; ++sb) {
 #pragma unroll
                     for (int k = 0; k < R; ++k) e[k][sb][0] = e[k][sb][1] = e[k][sb][2] = e[k][sb][3] = 0.f;
+                    [[maybe_unused]] float low[kParts == 2 ? R : 1][4] = {};  // of the second parts
 #pragma unroll
                     for (int i = 0; i < G::kKLoads; ++i) {
                         uint32_t w[2][G::kKBytes / 4];
@@ -530,26 +546,39 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                             codes_to_half<CODE>(w[0][y], a[0], a[2]);
                             codes_to_half<CODE>(w[1][y], a[1], a[3]);
 #pragma unroll
-                            for (int k = 0; k < R; ++k)
-#pragma unroll
-                                for (int z = 0; z < kParts; ++z) {
-                                    const uint32_t(&b)[2] = q.b[z][k][i * (G::kKBytes / 4) + y];
-                                    mma_f16(e[k][sb], a, b[0], b[1]);
-                                }
+                            for (int k = 0; k < R; ++k) {
+                                const int at = i * (G::kKBytes / 4) + y;
+                                mma_f16(e[k][sb], a, q.b[0][k][at][0], q.b[0][k][at][1]);
+                                if constexpr (kParts == 2) mma_f16(low[k], a, q.b[1][k][at][0], q.b[1][k][at][1]);
+                            }
                         }
+                    }
+                    if constexpr (kParts == 2) {
+#pragma unroll
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) e[k][sb][y] += low[k][y];
                     }
                 }
             };
             scores();
             // to exponents x + log2 vs - m, -inf where a row does not attend
             float ks[G::kSub], lv[G::kSub], inv_vs[G::kSub];
+            [[maybe_unused]] float rest_vs[G::kSub];
 #pragma unroll
             for (int sb = 0; sb < G::kSub; ++sb) {
                 const float vs = vsc[sb];
                 const bool none = !full && vs < kMinScale;
                 ks[sb] = ksc[sb];
-                lv[sb] = none ? kNoValues : kParts == 2 ? log2f(vs) : sm100::lg2(vs);
-                inv_vs[sb] = none ? kNoValuesInv : __frcp_rn(vs);
+                if constexpr (kParts == 2) {  // vs = 2^lv * (1..2): the first exact in the exponent, the rest a factor
+                    const uint32_t bits = __float_as_uint(vs), ex = min(bits >> 23, 253u);
+                    lv[sb] = none ? kNoValues : (float)((int)ex - 127);
+                    inv_vs[sb] = none ? kNoValuesInv : __uint_as_float((254u - ex) << 23);
+                    rest_vs[sb] = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) * kLift<T>;
+                } else {
+                    lv[sb] = none ? kNoValues : sm100::lg2(vs);
+                    inv_vs[sb] = none ? kNoValuesInv : __frcp_rn(vs);
+                }
             }
             auto exponents = [&](bool from_zero) {
 #pragma unroll
@@ -591,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
             float most = -INFINITY;
 #pragma unroll
             for (int k = 0; k < R; ++k) most = sm100::fmax3(most, top_of(k, 0), top_of(k, 1));
-            if (__any_sync(0xffffffffu, most > kRescaleAt)) {
+            if (__any_sync(0xffffffffu, most > kMoveAt<T>)) {
                 scores();  // again: the exponents took their place
                 exponents(true);
 #pragma unroll
@@ -602,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                         float top = top_of(k, y);
 #pragma unroll
                         for (int z = 4; z < 32; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
-                        m[y] = top - st.m[k][y] > kRescaleAt ? top - kHeadroom : st.m[k][y];
+                        const float to = kParts == 2 ? floorf(top) : top - kHeadroom;
+                        m[y] = top - st.m[k][y] > kMoveAt<T> ? to : st.m[k][y];
                     }
                     st.scale(k, ex2(st.m[k][0] - m[0]), ex2(st.m[k][1] - m[1]));
                     st.m[k][0] = m[0];
@@ -631,7 +661,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                 for (int k = 0; k < R; ++k)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = e[k][sb][2 * x], p1 = e[k][sb][2 * x + 1];
+                        float p0 = e[k][sb][2 * x], p1 = e[k][sb][2 * x + 1];
+                        if constexpr (kParts == 2) {
+                            p0 *= rest_vs[sb];
+                            p1 *= rest_vs[sb];
+                        }
                         const uint32_t h = half_pair(p0, p1);
                         pb[0][k][x] = transpose8(h);
                         if constexpr (kParts == 2) pb[1][k][x] = transpose8(half_rest(p0, p1, h, kRestScale));
@@ -656,13 +690,22 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
                         uint32_t a[4];
                         codes_to_half<CODE>(__byte_perm(v[0][y], v[1][y], pick), a[0], a[1]);
                         codes_to_half<CODE>(__byte_perm(v[2][y], v[3][y], pick), a[2], a[3]);
+                        if constexpr (kParts == 1) {
 #pragma unroll
-                        for (int k = 0; k < R; ++k) mma_f16(st.o[k][2 * y + z], a, pb[0][k][0], pb[0][k][1]);
-                        if constexpr (kParts == 2) {
+                            for (int k = 0; k < R; ++k) mma_f16(st.o[k][2 * y + z], a, pb[0][k][0], pb[0][k][1]);
+                        } else {  // on their own first: the products' accumulation truncates, these sums round
+                            float t[R][4] = {};
+                            uint32_t r[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) a[x] = rest_codes(a[x]);
+                            for (int x = 0; x < 4; ++x) r[x] = rest_codes(a[x]);
 #pragma unroll
-                            for (int k = 0; k < R; ++k) mma_f16(st.o[k][2 * y + z], a, pb[1][k][0], pb[1][k][1]);
+                            for (int k = 0; k < R; ++k) mma_f16(t[k], r, pb[1][k][0], pb[1][k][1]);
+#pragma unroll
+                            for (int k = 0; k < R; ++k) mma_f16(t[k], a, pb[0][k][0], pb[0][k][1]);
+#pragma unroll
+                            for (int k = 0; k < R; ++k)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) st.o[k][2 * y + z][x] += t[k][x];
                         }
                     }
             }
@@ -779,7 +822,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_fwd_cache_join(CacheFwdParams 
             const int q = r / p.G, h = t.hk * p.G + r % p.G;
             const float l = e ? l1 : l0;
             const bool there = in_tile < t.rows && l != 0.f;
-            const float inv = there ? 1.f / l : 0.f;
+            const float inv = there ? 1.f / (kLift<T> * l) : 0.f;
             const float a = there ? (e ? o.y : o.x) * inv : 0.f, b = there ? (e ? o.w : o.z) * inv : 0.f;
             T* out = static_cast<T*>(p.out) + t.b * p.o_sb + h * p.o_sh + q * p.o_sn + Geo<D>::kVBytes * g + 2 * i;
             if constexpr (std::is_same<T, float>::value)

@@ -132,6 +132,33 @@ def test_tokens_that_outweigh_the_others_of_whole_sequences(rows, real):
     assert bool(((lse.double().cpu().view(B, H, m) - want_lse).abs() <= tol_lse).all())
 
 
+@pytest.mark.parametrize("code", ["i8", "e4m3"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_fp32_queries_keep_their_bits(d, code):
+    """The error of out in its norm, against twice what single roundings of a weight come to.
+
+    In units u = 2^-24; a rounding by at most r u has a standard deviation of 0.58 r u, and errors of the weights
+    that are independent move out by their standard deviation, since out itself is such a sum. A score (about 1
+    in base e where the weights are large): d / 16 products in a row, each truncated by up to 2 u, on average u,
+    of a sum that grows to the score: 0.6 u d / 16 in all, to one side. Two roundings of its factor: 1.2 u; of
+    the exponent, below 4 where it counts: 0.8 u; the exponential (2^-22.5): 1.6 u; the weight times the rest of
+    its scale and its second part: u; sums of 16 values, truncated twice, and of those sums: 1.5 u. The squares
+    of the latter add up to less than 8 u^2. Accumulating all of P V in the products (8000 / 16 truncations to
+    one side, shared among some pieces) or an exponent around 10 (4 u more) does not keep within this."""
+    dtype, g = CODES[code], torch.Generator().manual_seed(50 + d)
+    n, H = [8000, 5000], 8
+    codes, scales, table = ref.make_cache(g, 2, H, 64, d, n, dtype)
+    q = torch.randn((2, H, 1, d), generator=g)
+    out, _ = sp.spattn_fwd_cache(q.cuda(), dev_cache(codes, scales, table, dtype), ints(n).cuda())
+    off = norm = 0.0
+    for b in range(2):
+        k, v = (ref.tokens(c, s, table, b, n[b], dtype) for c, s in zip(codes, scales))
+        want = torch.softmax(q[b].double() @ k.transpose(1, 2) / math.sqrt(d), -1) @ v
+        off += float((out[b].double().cpu() - want).square().sum())
+        norm += float(want.square().sum())
+    assert math.sqrt(off / norm) <= 2 * 2.0 ** -24 * math.sqrt((0.6 * d / 16) ** 2 + 8), math.sqrt(off / norm)
+
+
 @pytest.mark.parametrize("real", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", ROWS)
 def test_pages_that_are_missing(rows, real):
