@@ -439,9 +439,9 @@ __device__ __forceinline__ void produce(const CUtensorMap& k_map, const CUtensor
     int stage = 0;
     uint32_t phase = 1;  // the first round's waits pass at once
     bool dead = false;
+    int issued = 0;  // stages, up to S
     while (now.more) {
-        if (!dead && !sm100::mbar_wait_bounded(empty_at + 8 * stage, phase, kCacheWaitCycles)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
+        dead = !__all_sync(0xffffffffu, sm100::mbar_wait_bounded(empty_at + 8 * stage, phase, kCacheWaitCycles));
         if (dead) break;
         const unsigned there = __ballot_sync(0xffffffffu, now.raw >= 0);
         const uint32_t bar = full_at + 8 * stage;
@@ -461,12 +461,21 @@ __device__ __forceinline__ void produce(const CUtensorMap& k_map, const CUtensor
         if (lane == 0) sm100::mbar_expect_tx(bar, 2 * G::kBox * __popc(there));
         stage = stage + 1 == S ? 0 : stage + 1;
         phase ^= stage == 0;
+        issued = issued < S ? issued + 1 : S;
         now = next;
         next = after;
         ks = ks_next;
         vs = vs_next;
     }
-    if (dead && lane == 0) atomicOr(p.c.err, kErrTimeout);
+    // No copy is on its way when the block's shared memory goes to another: the computing warps wait for
+    // every stage, but not once one of their waits ran out. The last S stages, newest first (their full
+    // barriers' phases are those of the round that filled them).
+    for (int x = 0; x < issued; ++x) {
+        if (stage == 0) phase ^= 1;
+        stage = stage == 0 ? S - 1 : stage - 1;
+        dead |= !sm100::mbar_wait_bounded(full_at + 8 * stage, phase ^ 1, kCacheWaitCycles);
+    }
+    if (__any_sync(0xffffffffu, dead) && lane == 0) atomicOr(p.c.err, kErrTimeout);
 }
 
 template <typename T, int CODE, int D, int R>
@@ -756,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
         }
         part.close(p);
     }
-    if (dead && lane == 0) atomicOr(p.c.err, kErrTimeout);
+    if (dead) atomicOr(p.c.err, kErrTimeout);  // any lane's: it went on with what the ring held before
 }
 
 // Block x: the segment that block x of the other kernel began and others went on
