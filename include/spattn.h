@@ -383,6 +383,7 @@ int spattn_fwd_noalloc(const spattn_tensor* q, const spattn_tensor* k, const spa
  *               read. An entry outside [0, num_pages) that a call does need is
  *               left out (its tokens are not written, read as zeros, not
  *               attended to) and raises device error flag bit 2.
+ *   max_pages * page is at most 2^31 - 1024.
  * Sequences may share pages that are only read (a common prefix). Pages that a
  * call writes must each belong to one sequence: two that write the same page in
  * one call leave its codes unspecified. */

@@ -18,6 +18,9 @@ namespace spattn {
 constexpr int kCodeI8 = 0;
 constexpr int kCodeE4m3 = 1;
 constexpr int kMinPage = 16, kMaxPage = 256;
+// Tokens of a sequence: the attention's token numbers are 32-bit and run on to the end of a step of
+// up to 448 tokens, and to the one behind it.
+constexpr int64_t kMaxCacheTokens = 0x7fffffff - 1023;
 
 // Device error flag bits of the cache calls, beside those of spattn_internal.cuh. (That
 // header is part of what the other kernels' profiles are hashed over: it stays as it is.)

@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, D, R>())
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const int row = 8 * k + 2 * c + y;
-                            const int pos = row < t.rows ? t.base + (t.first_row + row) / p.G : -1;
+                            const int pos = row < t.rows ? max(t.base + (t.first_row + row) / p.G, -1) : -1;
 #pragma unroll
                             for (int sb = 0; sb < G::kSub; ++sb)
 #pragma unroll

@@ -360,7 +360,7 @@ __device__ __forceinline__ void softmax_role(const CacheFwdParams& p, TileShared
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        const int pos = valid ? t.base + row / p.G : -1;
+        const int pos = valid ? max(t.base + row / p.G, -1) : -1;  // (so that pos - window stays in range)
         // tokens that every row of this half attends to
         const int half_rows = t.rows - 128 * half < 128 ? t.rows - 128 * half : 128;
         const int lo_pos = t.base + (t.first_row + 128 * half) / p.G, hi_pos = t.base + (t.first_row + 128 * half + half_rows - 1) / p.G;

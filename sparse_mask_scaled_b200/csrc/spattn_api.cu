@@ -1427,8 +1427,8 @@ int check_cache(const spattn_cache* c, CacheView* v, int* code, int* d) {
                     (long long)sh[2], kMinPage, kMaxPage);
     if (c->batch < 0 || c->max_pages < 1)
         return fail(SPATTN_ERR_INVALID_ARG, "cache batch %d, max_pages %d", c->batch, c->max_pages);
-    if ((int64_t)c->max_pages * sh[2] > 0x7ffffffe)
-        return fail(SPATTN_ERR_UNSUPPORTED, "max_pages * page above 2^31 - 2 tokens");
+    if ((int64_t)c->max_pages * sh[2] > kMaxCacheTokens)
+        return fail(SPATTN_ERR_UNSUPPORTED, "max_pages * page above 2^31 - 1024 tokens");
     if ((int64_t)c->batch * sh[1] > 0x7fffffff) return fail(SPATTN_ERR_UNSUPPORTED, "batch * Hk too large");
     if (!c->page_table) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table is NULL");
     if (((uintptr_t)c->page_table) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table not aligned");

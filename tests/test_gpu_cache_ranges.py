@@ -161,6 +161,27 @@ def test_fp32_queries_keep_their_bits(d, code):
 
 @pytest.mark.parametrize("real", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", ROWS)
+def test_a_sequence_of_the_most_tokens(rows, real):
+    """2^31 - 1024 tokens under a window, over eight pages again and again: the same as a short sequence that
+    ends at the same place of the same page. The sequence beside it has fewer tokens than queries, and a
+    window that reaches as far before its first token as an int does."""
+    (H, Hk, m), dtype, g = rows, torch.int8, torch.Generator().manual_seed(46)
+    n, short, page = 2 ** 31 - 1024, 5120, 256
+    codes, scales, some = ref.make_cache(g, 1, Hk, page, 32, [8 * page], dtype)
+    row = some[0, :8]
+    table = row.repeat(n // page // 8 + 1)[None, :n // page].contiguous()
+    q = torch.randn((1, H, m, 32), generator=g).to(REAL[real])
+    kw = dict(window=700, n_global=40)
+    cache = dev_cache(codes, scales, table, dtype)
+    out, lse = sp.spattn_fwd_cache(q.cuda(), cache, ints([n]).cuda(), **kw)
+    want, want_lse, tol, tol_lse = cache_exact.attend(q, codes, scales, row.repeat(3)[None, :], [short], [m], dtype, **kw)
+    assert bool(((out.double().cpu() - want).abs() <= tol).all())
+    assert bool(((lse.double().cpu().view(want_lse.shape) - want_lse).abs() <= tol_lse).all())
+    assert check(q, codes, scales, row[None, :], [min(m, 5)], dtype, window=2 ** 31 - 1) == 0
+
+
+@pytest.mark.parametrize("real", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", ROWS)
 def test_pages_that_are_missing(rows, real):
     (H, Hk, m), dtype, g = rows, torch.float8_e4m3fn, torch.Generator().manual_seed(43)
     codes, scales, table = ref.make_cache(g, 2, Hk, 16, 64, [330, 200], dtype)
