@@ -386,7 +386,8 @@ int spattn_fwd_noalloc(const spattn_tensor* q, const spattn_tensor* k, const spa
  *   max_pages * page is at most 2^31 - 1024.
  * Sequences may share pages that are only read (a common prefix). Pages that a
  * call writes must each belong to one sequence: two that write the same page in
- * one call leave its codes unspecified. */
+ * one call leave its codes unspecified. A call of no sequence (batch 0) or of no
+ * token (m 0) does nothing; its arrays may then be NULL. */
 typedef struct {
     spattn_tensor k, v;
     float* k_scale;

@@ -1430,7 +1430,7 @@ int check_cache(const spattn_cache* c, CacheView* v, int* code, int* d) {
     if ((int64_t)c->max_pages * sh[2] > kMaxCacheTokens)
         return fail(SPATTN_ERR_UNSUPPORTED, "max_pages * page above 2^31 - 1024 tokens");
     if ((int64_t)c->batch * sh[1] > 0x7fffffff) return fail(SPATTN_ERR_UNSUPPORTED, "batch * Hk too large");
-    if (!c->page_table) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table is NULL");
+    if (!c->page_table && c->batch > 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table is NULL");
     if (((uintptr_t)c->page_table) % 4 != 0) return fail(SPATTN_ERR_INVALID_ARG, "cache.page_table not aligned");
     if (c->batch > 1 && c->table_stride < c->max_pages)
         return fail(SPATTN_ERR_INVALID_ARG, "cache.table_stride %lld < max_pages %d", (long long)c->table_stride,
@@ -1457,6 +1457,12 @@ constexpr int kCacheTileRows = 32;
 int check_cache_rows(const spattn_tensor* t, const char* name, const CacheView& v, int64_t heads, int64_t m, int d,
                      int32_t dtype) {
     const int64_t shape[4] = {v.B, heads, m, d};
+    spattn_tensor empty;
+    if (t && !t->data && v.B * m == 0) {  // an empty tensor has no address
+        empty = *t;
+        empty.data = reinterpret_cast<void*>(16);  // never used
+        t = &empty;
+    }
     return check_qkv(t, name, shape, dtype);
 }
 
@@ -2051,7 +2057,7 @@ int spattn_fwd_cache(const spattn_tensor* q, const spattn_cache* cache, const in
         return fail(SPATTN_ERR_UNSUPPORTED, "q batch, heads or tokens too large");
     if ((r = check_cache_rows(q, "q", p.c, H, m, d, q->dtype))) return r;
     if ((r = check_cache_rows(out, "out", p.c, H, m, d, q->dtype))) return r;
-    if (!seqlen) return fail(SPATTN_ERR_INVALID_ARG, "seqlen is NULL");
+    if (!seqlen && p.c.B > 0) return fail(SPATTN_ERR_INVALID_ARG, "seqlen is NULL");
     if ((r = check_lens(seqlen, "seqlen"))) return r;
     if ((r = check_lens(qlen, "qlen"))) return r;
     if (n_global < 0) return fail(SPATTN_ERR_INVALID_ARG, "n_global < 0");

@@ -3,7 +3,7 @@ device work."""
 import pytest
 
 import sparse_mask_scaled_b200 as sp
-from test_cache_cpu import D, HK, PAGE, UNSUPPORTED, cache, call, desc
+from test_cache_cpu import D, HK, INVALID, PAGE, UNSUPPORTED, cache, call, desc
 
 
 def empty_batch(name, c):
@@ -20,3 +20,21 @@ def test_a_table_may_hold_tokens_up_to_2_31_less_1024(name):
     assert st == sp.SPATTN_OK
     st, msg = empty_batch(name, cache(max_pages=most + 1, table_stride=most + 1))
     assert st == UNSUPPORTED and "max_pages" in msg
+
+
+@pytest.mark.parametrize("name", ["write", "read", "attend"])
+@pytest.mark.parametrize("batch,m", [(0, 4), (3, 0), (0, 0)])
+def test_calls_with_nothing_to_do(name, batch, m):
+    # empty tensors have no address
+    c = cache(batch=batch, page_table=None if batch == 0 else 0x300000)
+    st, msg = call(name, c, desc((batch, HK, m, D), sp.SPATTN_BF16, data=None), lens=None if batch == 0 else 0x400000)
+    assert st == sp.SPATTN_OK, msg
+    # what they are is checked all the same
+    assert call(name, c, desc((batch, HK, m, D), sp.SPATTN_I8, data=None))[0] == UNSUPPORTED
+    assert call(name, c, desc((batch, HK, m, 2 * D), sp.SPATTN_BF16, data=None))[0] == INVALID
+
+
+@pytest.mark.parametrize("name", ["write", "read", "attend"])
+def test_addresses_are_needed_where_there_is_something_to_do(name):
+    assert call(name, cache(page_table=None), desc((3, HK, 1, D), sp.SPATTN_BF16))[0] == INVALID
+    assert call(name, cache(), desc((3, HK, 1, D), sp.SPATTN_BF16, data=None))[0] == INVALID
