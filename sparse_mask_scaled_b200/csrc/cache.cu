@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kOneWarp ? 128 : 1024, kOneWarp ? 8 : 1)
     }
 #pragma unroll
     for (int y = 16; y > 0; y >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-    if constexpr (!kOneWarp) {
+    if constexpr (kOneWarp) {
+        __syncwarp();  // every lane has read the scale (an exchange of values orders no memory)
+    } else {
         if ((threadIdx.x & 31) == 0) s_amax[threadIdx.x >> 5] = amax;
         __syncthreads();  // and every thread has read the scale
         for (int y = 0; y < (int)(blockDim.x >> 5); ++y) amax = fmaxf(amax, s_amax[y]);
