@@ -549,6 +549,8 @@ def _call(fn, cache: Cache, stream, *args):
     """fn(*args, stream) with the cache's device current; stream: by default that
     device's current one."""
     import torch
+    if cache.device.type != "cuda":
+        raise ValueError(f"the cache is on {cache.device}; its calls need a CUDA device")
     if stream is None:  # a token's step is a few microseconds: no Stream object for its address
         s = torch._C._cuda_getCurrentRawStream(cache.device.index)
     else:
