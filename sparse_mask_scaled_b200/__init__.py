@@ -594,8 +594,15 @@ def spattn_fwd_cache(q, cache: Cache, seqlen, qlen=None, window: int = -1, n_glo
     tensors). ``window`` >= 0: only the last window + 1 tokens and the first
     ``n_global``. Returns (out [batch, H, m, d], lse [batch*H*m] or None)."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    dq = _beside(q, "q", cache)
+    if lse is not None:
+        rows = q.shape[0] * q.shape[1] * q.shape[2]
+        if lse.dtype != cache.k_scale.dtype or lse.numel() != rows or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of {rows} elements (batch * H * m)")
+        if lse.device != cache.device:
+            raise ValueError(f"lse is on {lse.device}, the cache on {cache.device}")
     out, lse = _outputs(q, out, lse, want_lse)
-    dq, do = _beside(q, "q", cache), _beside(out, "out", cache)
+    do = _beside(out, "out", cache)
     _call(LIB.spattn_fwd_cache, cache, stream, dq, cache.desc, _lens(seqlen, "seqlen", cache),
           _lens(qlen, "qlen", cache), window, n_global, scale, do, _ptr(lse))
     return out, lse

@@ -20,3 +20,19 @@ def test_a_cache_in_host_memory():
                  lambda: sp.spattn_fwd_cache(x, c, ints()), lambda: sp.spattn_cache_write(x, x, c, stream=0)):
         with pytest.raises(ValueError, match="cpu"):
             call()
+
+
+@pytest.mark.parametrize("lse", [
+    torch.zeros(7), torch.zeros(9), torch.zeros(8, dtype=torch.float64), torch.zeros(8, dtype=torch.bfloat16),
+    torch.zeros((2, 4, 2))[..., 0], torch.zeros(8, device="meta"),
+])
+def test_an_lse_that_cannot_hold_the_rows(lse):
+    c, q = make(), torch.zeros((2, 4, 1, 32))
+    with pytest.raises(ValueError, match="lse"):
+        sp.spattn_fwd_cache(q, c, ints(), lse=lse)
+
+
+@pytest.mark.parametrize("lse", [torch.zeros(8), torch.zeros((2, 4, 1))])
+def test_an_lse_of_the_right_size_passes(lse):
+    with pytest.raises(ValueError, match="cpu"):        # on to the next refusal
+        sp.spattn_fwd_cache(torch.zeros((2, 4, 1, 32)), make(), ints(), lse=lse)
