@@ -595,6 +595,9 @@ def spattn_fwd_cache(q, cache: Cache, seqlen, qlen=None, window: int = -1, n_glo
     ``n_global``. Returns (out [batch, H, m, d], lse [batch*H*m] or None)."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
     dq = _beside(q, "q", cache)
+    for name, x in (("window", window), ("n_global", n_global)):
+        if x != int(x) or not -1 << 31 <= x < 1 << 31:  # ctypes would pass on the low 32 bits
+            raise ValueError(f"{name} must be a 32-bit whole number, not {x}")
     if lse is not None:
         rows = q.shape[0] * q.shape[1] * q.shape[2]
         if lse.dtype != cache.k_scale.dtype or lse.numel() != rows or not lse.is_contiguous():
@@ -604,7 +607,7 @@ def spattn_fwd_cache(q, cache: Cache, seqlen, qlen=None, window: int = -1, n_glo
     out, lse = _outputs(q, out, lse, want_lse)
     do = _beside(out, "out", cache)
     _call(LIB.spattn_fwd_cache, cache, stream, dq, cache.desc, _lens(seqlen, "seqlen", cache),
-          _lens(qlen, "qlen", cache), window, n_global, scale, do, _ptr(lse))
+          _lens(qlen, "qlen", cache), int(window), int(n_global), scale, do, _ptr(lse))
     return out, lse
 
 

@@ -36,3 +36,17 @@ def test_an_lse_that_cannot_hold_the_rows(lse):
 def test_an_lse_of_the_right_size_passes(lse):
     with pytest.raises(ValueError, match="cpu"):        # on to the next refusal
         sp.spattn_fwd_cache(torch.zeros((2, 4, 1, 32)), make(), ints(), lse=lse)
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 31), dict(window=2 ** 32 + 5), dict(window=-2 ** 31 - 1),
+                                dict(n_global=2 ** 31), dict(n_global=2 ** 32), dict(window=1.5)])
+def test_numbers_that_no_int32_holds(kw):
+    # they went on as their low 32 bits: a window of 2^32 + 5 as one of 5
+    with pytest.raises((ValueError, TypeError), match="window|n_global"):
+        sp.spattn_fwd_cache(torch.zeros((2, 4, 1, 32)), make(), ints(), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 31 - 1), dict(window=-2 ** 31), dict(window=5, n_global=2 ** 31 - 1)])
+def test_the_largest_numbers_pass(kw):
+    with pytest.raises(ValueError, match="cpu"):        # on to the next refusal
+        sp.spattn_fwd_cache(torch.zeros((2, 4, 1, 32)), make(), ints(), **kw)
