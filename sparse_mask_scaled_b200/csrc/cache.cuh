@@ -57,16 +57,6 @@ __device__ __forceinline__ int64_t cache_capacity(const CacheView& c) {
 }
 
 template <int CODE>
-__device__ __forceinline__ float code_value(unsigned byte) {
-    if constexpr (CODE == kCodeI8) {
-        return (float)(int8_t)byte;
-    } else {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
-        return __half2float(__half(h));
-    }
-}
-
-template <int CODE>
 constexpr float code_max() {
     return CODE == kCodeI8 ? 127.f : 448.f;
 }
