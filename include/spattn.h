@@ -385,8 +385,8 @@ int spattn_fwd_noalloc(const spattn_tensor* q, const spattn_tensor* k, const spa
  *               attended to) and raises device error flag bit 2.
  *   max_pages * page is at most 2^31 - 1024.
  * Sequences may share pages that are only read (a common prefix). Pages that a
- * call writes must each belong to one sequence: two that write the same page in
- * one call leave its codes unspecified. A call of no sequence (batch 0) or of no
+ * call writes must each belong to one sequence and stand once in its row: two
+ * places that write the same page in one call leave its codes unspecified. A call of no sequence (batch 0) or of no
  * token (m 0) does nothing; its arrays may then be NULL. */
 typedef struct {
     spattn_tensor k, v;
@@ -423,9 +423,9 @@ int spattn_cache_write(const spattn_tensor* k, const spattn_tensor* v, const spa
  * values of the places start[b] + t, t < length[b], rounded to nearest even, and
  * zeros for t >= length[b] and for places without a page (which raise device
  * error flag bit 2). start, length as spattn_cache_write's. The values are what
- * spattn_fwd_cache attends to; with k and v given to spattn_fwd_mask_kpad a
- * whole cached sequence can run under any mask. Stream-ordered, never
- * synchronises, allocates nothing. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * spattn_fwd_cache attends to (but for V scales at the ends of the fp32 range, see
+ * there); with k and v given to spattn_fwd_mask_kpad a whole cached sequence can run
+ * under any mask. Stream-ordered, never synchronises, allocates nothing. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int spattn_cache_read(const spattn_cache* cache, const int32_t* start, const int32_t* length,
                       const spattn_tensor* k, const spattn_tensor* v, void* stream);
 
@@ -480,7 +480,8 @@ int spattn_device_error(void* stream, uint32_t* flags);
  * device-side wait expired, SPATTN_ERR_BAD_CSR if a column outside [0, n) was
  * skipped (or an asynchronous build met a negative half-width),
  * SPATTN_ERR_BAD_CACHE if a cache call left out places or met values it cannot
- * hold (bits 2 and 3 of spattn_device_error), SPATTN_OK otherwise (SPATTN_ERR_CUDA if the synchronisation itself fails). */
+ * hold (bits 2 and 3 of spattn_device_error), SPATTN_OK otherwise (SPATTN_ERR_CUDA
+ * if the synchronisation itself fails). */
 int spattn_check_device_error(void* stream);
 
 /* Library version: major * 10000 + minor * 100 + patch. */

@@ -8,11 +8,14 @@
 // and where s grew the older tokens' codes become round((c * s_old) / s). Both
 // quotients are IEEE fp32 quotients, so that the codes are a function of the
 // inputs alone; a division is only made where the product with 1 / s lies so near
-// a rounding border that it could round the other way. Bound: HBM (values in,
-// codes out).
+// a rounding border that it could round the other way. HBM (values in, codes
+// out) would take 19 us of the 46 us that 8 prompts of up to 4096 tokens take
+// (8 heads, d = 128, bf16 to e4m3): what bounds it is issue, 72 % of the time,
+// about 25 instructions a value.
 //
 // Read. A thread turns 16 bytes' worth of values of several tokens, all loads
-// before the first use. Bound: HBM.
+// before the first use. Bound: HBM (4 x up to 16384 tokens: 119 us on the device, 93 %
+// of the measured copy rate).
 #include "cache.cuh"
 
 namespace spattn {
@@ -361,8 +364,8 @@ cudaError_t write_d(const CacheView& c, const CacheRows& r, cudaStream_t s) {
         k_cache_write<T, CODE, D, 4, true><<<(unsigned)((items + 3) / 4), 128, 0, counted(s)>>>(c, r, slots, items);
         return cudaGetLastError();
     }
-    // eight vectors a thread: the kernel issues instructions 82 % of the time with two, for what is done
-    // once a thread (place, scale, reduction); smaller pages fill a warp with four
+    // eight vectors a thread share what is done once a thread (place, scale, reduction): 90 us with two,
+    // 79 with eight, for 8 prompts written and read back; smaller pages fill a warp with four
     const int vecs = page * D / V;  // 256..8192 here
     if (vecs >= 512)
         k_cache_write<T, CODE, D, 8, false><<<(unsigned)items, vecs / 8, 0, counted(s)>>>(c, r, slots, items);

@@ -32,7 +32,10 @@
 // goes into the exponent; the rest is a factor of the weight. The error against 64 bits
 // is 0.2 to 0.3e-6 of out where torch operations in fp32 have 0.2 to 0.9e-6.
 //
-// Streaming. The kernel is bound by HBM at long caches: each code is read once.
+// Streaming. Each code is read once; HBM is what the kernel cannot do without. It
+// gets 5.2 TB/s of it (two sequences of 131071 tokens, d = 128, int8: 104 us): 14
+// computing warps an SM wait for loads from shared memory and for their own chains
+// of conversions, products and exponentials, and issue slots are busy 53 % of the time.
 // A producer warp fills a ring in shared memory by TMA: a copy brings 16 tokens
 // of one page (4-D map {d, token, head, page}, any strides), swizzled so that the
 // fragment loads meet few bank conflicts; a stage is kSub such sub-blocks of K and
@@ -311,7 +314,11 @@ __device__ __forceinline__ void write_piece(float* ws, const State<D, R>& s, int
     }
 }
 // Blocks an SM holds: with 128 registers a thread two, else one. O, Q and the
-// scores take `held` of them.
+// scores take `held` of them. Two blocks are faster up to 68, though some of those
+// builds spill (the second number: one block; 16 sequences of 8192 tokens at d = 128,
+// of 16384 below): bf16 d = 64 R = 2 83 / 113 us, d = 32 R = 2 70 / 95 us, fp32 d = 128
+// R = 1 74 / 82 us, d = 32 R = 2 85 / 103 us. From 80 on they are not: fp32 d = 64
+// R = 2 75 / 72 us, bf16 d = 32 R = 3 120 / 103 us, d = 64 R = 3 123 / 119 us.
 template <typename T, int D, int R>
 constexpr int blocks_per_sm() {
     const int held = (D / 4 + parts<T>() * D / 8 + 4 * Geo<D>::kSub) * R;

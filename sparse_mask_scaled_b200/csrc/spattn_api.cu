@@ -1450,7 +1450,14 @@ int check_cache(const spattn_cache* c, CacheView* v, int* code, int* d) {
     return SPATTN_OK;
 }
 
-// bf16 queries with more rows a K/V head than this take the tensor-core tiles.
+// bf16 queries with more rows a K/V head than this take the tensor-core tiles, which cost
+// a step of 256 rows whatever the rows; the streaming kernel takes its 8, 16, 24 or 32 rows at a
+// time. Streaming / tiles, us, 16 sequences of 8 K/V heads, e4m3:
+//   rows                    8         16         24         32         40         64         96        128
+//   d = 128,  8192    59/186     85/197     95/202    137/206    235/207    242/208    332/211    433/215
+//   d =  64, 16384    71/304     84/314    120/318    127/322    233/322    234/323    324/324    434/325
+//   d =  32, 16384    59/289     70/298    103/302    119/306    197/307    206/306    279/309    367/310
+// (Below d = 128 streaming would win up to 64 rows too: there this limit is too low.)
 constexpr int kCacheTileRows = 32;
 
 // A [batch, heads, m, d] tensor beside a cache.
